@@ -448,6 +448,134 @@ int moe_aux_loss(const float *logits, const int32_t *load, int64_t T, int64_t n_
                  int k, float coeff, float *aux_out, float *d_logits, void *ws, size_t ws_bytes,
                  void *stream);
 
+/*
+ * Routing by scores over all E experts.  The other form of a router beside
+ * moe_route's softmax over the k selected logits: every expert has a score,
+ *   score MOE_SCORE_SOFTMAX: s_e = exp(x_e) / sum_i exp(x_i)
+ *         MOE_SCORE_SIGMOID: s_e = 1 / (1 + exp(-x_e)),      x = logits[t,:],
+ * the experts compete by c_e = s_e + sel_bias[e] (sel_bias NULL: by x_e
+ * itself, which orders them as s_e does), and the weights are those of the
+ * selected scores without the bias:
+ *   topk_w[t,j] = scale * s_j / sum_i s_i  (renorm != 0; i over the k selected)
+ *                 scale * s_j              (renorm == 0).
+ * Groups: the experts form n_group groups of E / n_group consecutive ids; a
+ * group's value is its largest c_e (group_top 1) or the sum of its two
+ * largest (group_top 2; s_e in place of c_e without a bias), and only experts
+ * of the topk_group groups of largest value can be selected.  n_group 1, or
+ * topk_group = n_group: no restriction.
+ * Every comparison decides as arithmetic in 64 bits on the fp32 logits and
+ * bias does; equal values go to the lower id (group or expert), a NaN ranks
+ * below every number (in a group's value it counts as -inf).  topk_idx is in
+ * descending order of c_e.  Logits of -inf (masked experts) have score 0;
+ * with renorm, a selection of scores that are all 0 gets weights 0 (scores
+ * too small for fp32 still share the weight in proportion).  A NaN logit makes its own sigmoid score,
+ * or all softmax scores of its row, NaN, and +inf the softmax scores of its
+ * row; with renorm only what is selected matters.  sel_bias must be finite.
+ * 1 <= n_group <= 32 and a divisor of E; group_top 2 needs groups of two
+ * experts or more; k <= topk_group * E / n_group; scale positive and finite;
+ * T * k < 2^31; logits 16-byte aligned.  Outputs as moe_route's.
+ */
+#define MOE_SCORE_SOFTMAX 0
+#define MOE_SCORE_SIGMOID 1
+int moe_route_scored(const float *logits, const float *sel_bias, int64_t T, int E, int k,
+                     int score, int n_group, int topk_group, int group_top, int renorm,
+                     float scale, int32_t *topk_idx, float *topk_w, void *stream);
+
+/*
+ * Adjoint of moe_route_scored's weights with respect to the logits (the
+ * selection and the bias carry no gradient).  With g_j = d_row_scale[
+ * slot_to_row[t*k+j]] (0 for a negative row; slot_to_row NULL: g_j =
+ * d_row_scale[t*k+j]), w_j = topk_w[t,j], p_j = w_j / scale, m = sum_i p_i g_i:
+ *   d_topk_w[t,j] = g_j                                  (d_topk_w may be NULL)
+ *   d_logits[t,e] = 0 but, for e = topk_idx[t,j],
+ *     sigmoid, renorm:  w_j (1 - s_j) (g_j - m)     plain:  w_j (1 - s_j) g_j
+ *     softmax, renorm:  w_j (g_j - m)
+ *   softmax, plain (every e): -scale s_e m, and w_j g_j added at the selected.
+ * d_logits: [T,E] (out, fully written); it can be given to
+ * moe_router_logits_bwd and moe_permute_bwd_router.  score, renorm and scale
+ * as in the forward call; logits, d_logits 16-byte aligned; the two must not
+ * overlap.  A row whose weights are all 0 gets zeros.
+ */
+int moe_route_scored_bwd(const float *logits, const int32_t *topk_idx, const float *topk_w,
+                         const float *d_row_scale, const int32_t *slot_to_row, int64_t T, int E,
+                         int k, int score, int renorm, float scale, float *d_topk_w,
+                         float *d_logits, void *stream);
+
+/* ---------------------------------------------------------------- 8-bit experts */
+
+/*
+ * Expert products in 8-bit floating point with a scale for each block of 128.
+ * Values are e4m3 (OCP: largest 448, no infinity, NaN 0x7f / 0xff), one byte
+ * each.  A block's scale is a power of two 2^s, stored as the byte s + 127:
+ * s is the smallest integer >= -127 with (largest finite |x| of the block)
+ * <= 448 * 2^s, and 0 for a block without a finite nonzero value; the stored
+ * value is x * 2^-s rounded to e4m3 (nearest even).  NaN and infinities
+ * become NaN, so that they reach the result.
+ *  - Rows (activations) [R,K]: a scale per 128 consecutive k of a row,
+ *    [R, moe_fp8_scale_cols(K)] bytes.
+ *  - Weights [E,N,K]: a scale per 128 (n) x 128 (k),
+ *    [E, ceil(N/128), moe_fp8_scale_cols(K)] bytes.
+ * moe_fp8_scale_cols(K) = ceil(K/128) rounded up to a multiple of 4; the
+ * padding bytes hold 127 and no value depends on them.  All sizes are
+ * multiples of 16 from 16 to 65536; 1 <= E <= 1024; R < 2^31; pointers
+ * 16-byte aligned.  Products accumulate in fp32, after the matrix
+ * instruction has added each 8 consecutive k with at least 13 bits below the
+ * largest of their products.  Rows at or past offsets[E]
+ * are not read and not written.  Offsets that are no ascending sequence in
+ * [0,R] are clamped to it and give unspecified rows.
+ */
+int moe_fp8_scale_cols(int K);
+
+/* Rows x [R,K] (dtype MOE_BF16 or MOE_F32) to q [R,K] and scale. */
+int moe_quant_rows_fp8(const void *x, int dtype, int64_t R, int K, uint8_t *q, uint8_t *scale,
+                       void *stream);
+
+/*
+ * Expert weights w [E,N,K] (dtype MOE_BF16 or MOE_F32) to q [E,N,K] and scale.
+ * With qt and scale_t (both or neither NULL) also the transposed weights
+ * qt [E,K,N], scale_t [E, ceil(K/128), moe_fp8_scale_cols(N)]: the same
+ * values (a square block keeps its scale), laid out for the product that
+ * forms the gradient of the rows.
+ */
+int moe_quant_weights_fp8(const void *w, int dtype, int E, int N, int K, uint8_t *q,
+                          uint8_t *scale, uint8_t *qt, uint8_t *scale_t, void *stream);
+
+/*
+ * Grouped product over rows sorted by expert: for each expert e and each of
+ * its rows r in [offsets[e], offsets[e+1]), with A and B the values that
+ * bytes and scales stand for,
+ *   c[r,n] = bf16(row_scale[r] * sum_k A[r,k] B[e,n,k])   (row_scale NULL = 1).
+ * a [R,K], a_scale; or, with row_to_slot (as moe_permute writes it) and k,
+ * unpermuted token rows a [R/k, K]: row r reads token row_to_slot[r] / k
+ * (R a multiple of k, k <= 32, (R/k) * K < 2^31, R * k < 2^32; entries
+ * outside [0,R) read zeros).  row_to_slot NULL: k is ignored.  b [E,N,K],
+ * b_scale; c: [R,N] bf16 (out).  With the transposed weights of
+ * moe_quant_weights_fp8 and the quantised output gradient as a, c is the
+ * gradient of the rows.
+ */
+int moe_grouped_gemm_fp8(const uint8_t *a, const uint8_t *a_scale, const int32_t *row_to_slot,
+                         int k, const int32_t *offsets, int E, int64_t R, int N, int K,
+                         const uint8_t *b, const uint8_t *b_scale, const float *row_scale,
+                         void *c, void *stream);
+
+/*
+ * moe_grouped_ffn_fwd with 8-bit weights and activations (frozen experts:
+ * rollouts, serving).  Per row r of expert e:
+ *   [g | u] = X[r] . W_gu[e]^T      (fp32; gate rows 0..f-1, up rows f..2f-1)
+ *   h[r]    = 8 bits of silu(g) * u, as moe_quant_rows_fp8 (h, h_scale: out)
+ *   y_perm[r] = bf16(row_scale[r] * (H[r] . W_down[e]^T))
+ * x, x_scale: rows [R,d], or token rows with row_to_slot and k as above;
+ * w_gu [E,2f,d], w_gu_scale [E, ceil(2f/128), moe_fp8_scale_cols(d)];
+ * w_down [E,d,f], w_down_scale [E, ceil(d/128), moe_fp8_scale_cols(f)];
+ * h [R,f], h_scale [R, moe_fp8_scale_cols(f)]; y_perm [R,d] bf16.
+ */
+int moe_grouped_ffn_fwd_fp8(const uint8_t *x, const uint8_t *x_scale, const int32_t *row_to_slot,
+                            int k, const int32_t *offsets, int E, int64_t R, int d, int f,
+                            const uint8_t *w_gu, const uint8_t *w_gu_scale,
+                            const uint8_t *w_down, const uint8_t *w_down_scale,
+                            const float *row_scale, uint8_t *h, uint8_t *h_scale, void *y_perm,
+                            void *stream);
+
 /* ---------------------------------------------------------------- timing */
 
 /*
@@ -464,7 +592,8 @@ int moe_aux_loss(const float *logits, const int32_t *load, int64_t T, int64_t n_
  * route_topk_biased, expert_load, expert_load_reduce, bias_update, aux_loss,
  * aux_loss_final, lora_proj, lora_transpose, lora_grad,
  * gg_fwd_gate_up_swiglu_gather, gg_bwd_dh_dswiglu_gather, row_scale,
- * gg_bwd_dw_gate_up_gather.
+ * gg_bwd_dw_gate_up_gather, route_scored, route_scored_bwd, quant_rows_fp8,
+ * quant_weights_fp8, gg_fp8, gg_fp8_gate_up, gg_fp8_down.
  */
 int moe_timing_enable(int on);
 int moe_timing_reset(void);

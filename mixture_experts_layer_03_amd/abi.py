@@ -20,6 +20,8 @@ LIB_PATH = os.environ.get("MOE_LIBRARY") or os.path.join(
 MOE_OK = 0
 MOE_F32 = 0
 MOE_BF16 = 1
+MOE_SCORE_SOFTMAX = 0
+MOE_SCORE_SIGMOID = 1
 
 _c_void_p = ctypes.c_void_p
 _i32, _i64, _sz = ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
@@ -91,6 +93,22 @@ _SIGS = {
                                           _c_void_p, _c_void_p, _i32, _i32, _i32, _c_void_p,
                                           _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
                                           _c_void_p, _c_void_p, _c_void_p, _sz, _c_void_p]),
+    "moe_route_scored": (_i32, [_c_void_p, _c_void_p, _i64, _i32, _i32, _i32, _i32, _i32, _i32,
+                                _i32, ctypes.c_float, _c_void_p, _c_void_p, _c_void_p]),
+    "moe_route_scored_bwd": (_i32, [_c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _i64,
+                                    _i32, _i32, _i32, _i32, ctypes.c_float, _c_void_p, _c_void_p,
+                                    _c_void_p]),
+    "moe_fp8_scale_cols": (_i32, [_i32]),
+    "moe_quant_rows_fp8": (_i32, [_c_void_p, _i32, _i64, _i32, _c_void_p, _c_void_p, _c_void_p]),
+    "moe_quant_weights_fp8": (_i32, [_c_void_p, _i32, _i32, _i32, _i32, _c_void_p, _c_void_p,
+                                     _c_void_p, _c_void_p, _c_void_p]),
+    "moe_grouped_gemm_fp8": (_i32, [_c_void_p, _c_void_p, _c_void_p, _i32, _c_void_p, _i32, _i64,
+                                    _i32, _i32, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
+                                    _c_void_p]),
+    "moe_grouped_ffn_fwd_fp8": (_i32, [_c_void_p, _c_void_p, _c_void_p, _i32, _c_void_p, _i32,
+                                       _i64, _i32, _i32, _c_void_p, _c_void_p, _c_void_p,
+                                       _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
+                                       _c_void_p]),
     "moe_timing_enable": (_i32, [_i32]),
     "moe_timing_reset": (_i32, []),
     "moe_timing_query": (_i32, [ctypes.c_char_p, ctypes.POINTER(ctypes.c_double),
@@ -355,6 +373,62 @@ def moe_grouped_ffn_lora_bwd_saved(ws, R, E, d, f, r):
         off = int(p.value) - base
         out.append(ws[off:off + 2 * R * r].view(torch.bfloat16).view(R, r))
     return tuple(out)
+
+
+def moe_route_scored(logits, sel_bias, k, topk_idx, topk_w, score=MOE_SCORE_SOFTMAX, n_group=1,
+                     topk_group=1, group_top=1, renorm=True, scale=1.0, stream=None):
+    """sel_bias: [E] or None."""
+    T, E = logits.shape
+    _check("moe_route_scored", lib().moe_route_scored(
+        _p(logits), _p(sel_bias), T, E, k, score, n_group, topk_group, group_top,
+        1 if renorm else 0, float(scale), _p(topk_idx), _p(topk_w), _stream(stream)))
+
+
+def moe_route_scored_bwd(logits, topk_idx, topk_w, d_row_scale, slot_to_row, d_topk_w, d_logits,
+                         score=MOE_SCORE_SOFTMAX, renorm=True, scale=1.0, stream=None):
+    """slot_to_row None: d_row_scale is in slot order; d_topk_w may be None."""
+    T, E = logits.shape
+    k = topk_idx.shape[1]
+    _check("moe_route_scored_bwd", lib().moe_route_scored_bwd(
+        _p(logits), _p(topk_idx), _p(topk_w), _p(d_row_scale), _p(slot_to_row), T, E, k, score,
+        1 if renorm else 0, float(scale), _p(d_topk_w), _p(d_logits), _stream(stream)))
+
+
+def moe_fp8_scale_cols(K) -> int:
+    return int(lib().moe_fp8_scale_cols(K))
+
+
+def moe_quant_rows_fp8(x, q, scale, stream=None):
+    R, K = x.shape
+    _check("moe_quant_rows_fp8", lib().moe_quant_rows_fp8(
+        _p(x), _dtype_code(x), R, K, _p(q), _p(scale), _stream(stream)))
+
+
+def moe_quant_weights_fp8(w, q, scale, qt=None, scale_t=None, stream=None):
+    E, N, K = w.shape
+    _check("moe_quant_weights_fp8", lib().moe_quant_weights_fp8(
+        _p(w), _dtype_code(w), E, N, K, _p(q), _p(scale), _p(qt), _p(scale_t), _stream(stream)))
+
+
+def moe_grouped_gemm_fp8(a, a_scale, offsets, b, b_scale, row_scale, c, row_to_slot=None, k=1,
+                         stream=None):
+    """With row_to_slot, a holds token rows and row r reads token row_to_slot[r] / k."""
+    R = c.shape[0]
+    E, N, K = b.shape
+    _check("moe_grouped_gemm_fp8", lib().moe_grouped_gemm_fp8(
+        _p(a), _p(a_scale), _p(row_to_slot), k, _p(offsets), E, R, N, K, _p(b), _p(b_scale),
+        _p(row_scale), _p(c), _stream(stream)))
+
+
+def moe_grouped_ffn_fwd_fp8(x, x_scale, offsets, w_gu, w_gu_scale, w_down, w_down_scale,
+                            row_scale, h, h_scale, y_perm, row_to_slot=None, k=1, stream=None):
+    """With row_to_slot, x holds token rows and row r reads token row_to_slot[r] / k."""
+    R, d = y_perm.shape
+    E, _, f = w_down.shape
+    _check("moe_grouped_ffn_fwd_fp8", lib().moe_grouped_ffn_fwd_fp8(
+        _p(x), _p(x_scale), _p(row_to_slot), k, _p(offsets), E, R, d, f, _p(w_gu),
+        _p(w_gu_scale), _p(w_down), _p(w_down_scale), _p(row_scale), _p(h), _p(h_scale),
+        _p(y_perm), _stream(stream)))
 
 
 def moe_timing_enable(on: bool):

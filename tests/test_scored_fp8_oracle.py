@@ -1,0 +1,173 @@
+"""CPU pins of the oracle of the score routing and the 8-bit blocks, and the
+refusals of their entry points (no GPU)."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from mixture_experts_layer_03_amd import abi
+from oracle import scored_fp8 as S
+
+
+def _rng(seed):
+    return np.random.Generator(np.random.PCG64(seed))
+
+
+# ------------------------------------------------------------------ oracle
+
+@pytest.mark.parametrize("sigmoid,renorm", [(True, True), (True, False), (False, True), (False, False)])
+def test_weights_and_gradient_match_torch_and_differences(sigmoid, renorm):
+    r = _rng(3)
+    x = r.standard_normal((7, 24)) * 2
+    idx, w = S.route_scored(x, None, 5, sigmoid, renorm=renorm, scale=1.7)
+    t = torch.tensor(x, requires_grad=True)
+    s = torch.sigmoid(t) if sigmoid else torch.softmax(t, 1)
+    sel = s.gather(1, torch.tensor(idx.astype(np.int64)))
+    tw = 1.7 * (sel / sel.sum(1, keepdim=True) if renorm else sel)
+    assert np.allclose(w, tw.detach().numpy(), rtol=1e-13)
+    g = r.standard_normal((7, 5))
+    tw.backward(torch.tensor(g))
+    d = S.route_scored_bwd(x, idx, g, sigmoid, renorm, 1.7)
+    assert np.allclose(d, t.grad.numpy(), rtol=1e-11, atol=1e-14)
+    h = 1e-6
+    for e in range(24):
+        p, q = x.copy(), x.copy()
+        p[:, e] += h
+        q[:, e] -= h
+        num = ((S.weights(p, idx, sigmoid, renorm, 1.7) - S.weights(q, idx, sigmoid, renorm, 1.7)) * g).sum(1) / (2 * h)
+        assert np.allclose(d[:, e], num, atol=1e-8)
+
+
+def test_groups_and_ties_closed_form():
+    # two groups of three; group values by their largest, by the sum of their two largest
+    x = np.array([[2.0, 0.0, 0.0, 1.5, 1.5, -9.0]])
+    assert S.route_scored(x, None, 2, True, 2, 1, 1)[0].tolist() == [[0, 1]]
+    assert S.route_scored(x, None, 2, True, 2, 1, 2)[0].tolist() == [[3, 4]]
+    # a bias moves the choice, not the weights; equal choices go to the lower id
+    idx, w = S.route_scored(np.zeros((1, 4)), np.array([0.0, 0.5, 0.5, 0.0]), 3, True, renorm=False)
+    assert idx.tolist() == [[1, 2, 0]] and w.tolist() == [[0.5, 0.5, 0.5]]
+    # masked rows
+    idx, w = S.route_scored(np.full((1, 4), -np.inf), None, 2, True)
+    assert idx.tolist() == [[0, 1]] and w.tolist() == [[0.0, 0.0]]
+    idx, w = S.route_scored(np.full((1, 4), np.finfo(np.float32).min), None, 2, False)
+    assert w.tolist() == [[0.5, 0.5]]
+
+
+def test_e4m3_rounding_is_torchs():
+    r = _rng(5)
+    v = np.concatenate([r.standard_normal(20000) * np.exp2(r.integers(-12, 8, 20000)), S._POS, -S._POS,
+                        (S._POS[1:] + S._POS[:-1]) / 2, [0.0, -0.0]])
+    v = np.clip(v, -448, 448).astype(np.float32)
+    ref = torch.tensor(v).to(torch.float8_e4m3fn)
+    assert np.array_equal(S.to_e4m3(v), ref.view(torch.uint8).numpy())
+    got = torch.arange(256, dtype=torch.uint8).view(torch.float8_e4m3fn).double().numpy()
+    assert np.array_equal(S.e4m3_table(), got, equal_nan=True)
+
+
+def test_block_exponent_is_the_smallest_that_fits():
+    for a in np.concatenate([np.exp2(np.linspace(-118, 120, 239)), 448 * np.exp2(np.arange(-20.0, 20)),
+                             np.nextafter(448.0, 1e9) * np.exp2(np.arange(-20.0, 20))]):
+        s = int(S.block_exponent(a))
+        assert a <= 448 * 2.0 ** s and a > 448 * 2.0 ** (s - 1)
+    assert S.block_exponent(0.0) == 0 and S.block_exponent(1e-45) == -127
+
+
+def test_transposed_weights_hold_the_same_values():
+    w = _rng(6).standard_normal((2, 176, 304))
+    w[0, :100] *= 40
+    q, s = S.quant_weights(w)
+    qt, st = S.quant_weights(w.transpose(0, 2, 1))
+    for e in range(2):
+        assert np.array_equal(S.weight_values(q[e], s[e]).T, S.weight_values(qt[e], st[e]))
+
+
+# ------------------------------------------------------------------ refusals
+
+P = ctypes.c_void_p(0x1000)   # never dereferenced: validation fails first
+MIS = ctypes.c_void_p(0x1008)
+
+
+def _route(L, T=10, E=16, k=4, score=1, n_group=4, topk_group=2, group_top=2, renorm=1, scale=1.0,
+           logits=P, bias=P, idx=P, w=P):
+    return L.moe_route_scored(logits, bias, T, E, k, score, n_group, topk_group, group_top, renorm,
+                              ctypes.c_float(scale), idx, w, None)
+
+
+@pytest.mark.parametrize("change,rc", [
+    (dict(T=-1), -1), (dict(E=0), -2), (dict(E=1025), -2), (dict(k=0), -2), (dict(k=17), -2),
+    (dict(E=64, k=33, n_group=1, topk_group=1), -2), (dict(score=2), -2), (dict(score=-1), -2),
+    (dict(n_group=0), -2), (dict(n_group=3), -2), (dict(E=64, n_group=64, topk_group=8, group_top=1), -2),
+    (dict(topk_group=0), -2), (dict(topk_group=5), -2), (dict(group_top=0), -2), (dict(group_top=3), -2),
+    (dict(n_group=16, topk_group=8, group_top=2), -2), (dict(k=9), -2), (dict(scale=0.0), -1),
+    (dict(scale=-1.0), -1), (dict(scale=float("nan")), -1), (dict(scale=float("inf")), -1),
+    (dict(logits=None), -1), (dict(idx=None), -1), (dict(w=None), -1), (dict(logits=MIS), -1),
+    (dict(T=1 << 30), -2), (dict(T=0, logits=None, idx=None, w=None), 0)],
+    ids=lambda v: str(v).replace(" ", "") if isinstance(v, dict) else "")
+def test_route_scored_refuses(change, rc):
+    L = abi.lib()
+    assert _route(L, **change) == rc
+    assert (L.moe_last_error() == b"") == (rc == 0)
+
+
+def test_route_scored_bwd_refuses():
+    L = abi.lib()
+    f = ctypes.c_float(1.0)
+    ok = [P, P, P, P, P, 10, 16, 4, 1, 1, f, P, P, None]
+    for i, v, rc in [(0, None, -1), (1, None, -1), (2, None, -1), (3, None, -1), (12, None, -1), (0, MIS, -1),
+                     (12, MIS, -1), (5, -1, -1), (6, 0, -2), (7, 17, -2), (8, 5, -2), (10, ctypes.c_float(0), -1)]:
+        a = list(ok)
+        a[i] = v
+        assert L.moe_route_scored_bwd(*a) == rc, (i, v)
+    assert L.moe_route_scored_bwd(None, None, None, None, None, 0, 16, 4, 1, 1, f, None, None, None) == 0
+
+
+def test_quantisation_refuses():
+    L = abi.lib()
+    assert [L.moe_fp8_scale_cols(k) for k in (0, 16, 128, 129, 512, 513, 2880)] == [0, 4, 4, 4, 4, 8, 24]
+    ok = [P, 1, 10, 64, P, P, None]
+    for i, v, rc in [(0, None, -1), (4, None, -1), (5, None, -1), (0, MIS, -1), (4, MIS, -1), (5, MIS, -1), (1, 2, -2),
+                     (2, -1, -1), (2, 1 << 31, -2), (3, 0, -2), (3, 24, -2), (3, 65552, -2)]:
+        a = list(ok)
+        a[i] = v
+        assert L.moe_quant_rows_fp8(*a) == rc, (i, v)
+    assert L.moe_quant_rows_fp8(None, 1, 0, 64, None, None, None) == 0
+    ok = [P, 1, 2, 64, 64, P, P, P, P, None]
+    for i, v, rc in [(0, None, -1), (5, None, -1), (6, None, -1), (7, None, -1), (8, None, -1), (7, MIS, -1),
+                     (8, MIS, -1), (1, 3, -2), (2, 0, -2), (2, 1025, -2), (3, 8, -2), (4, 72, -2)]:
+        a = list(ok)
+        a[i] = v
+        assert L.moe_quant_weights_fp8(*a) == rc, (i, v)
+
+
+def test_products_refuse():
+    L = abi.lib()
+    # a, a_scale, row_to_slot, k, offsets, E, R, N, K, b, b_scale, row_scale, c, stream
+    ok = [P, P, P, 4, P, 8, 400, 64, 64, P, P, P, P, None]
+    bad = [(0, None, -1), (1, None, -1), (4, None, -1), (9, None, -1), (10, None, -1), (12, None, -1), (0, MIS, -1),
+           (1, MIS, -1), (9, MIS, -1), (10, MIS, -1), (12, MIS, -1), (3, 0, -2), (3, 33, -2), (3, 3, -1), (5, 0, -2),
+           (5, 1025, -2), (6, -1, -1), (6, 1 << 31, -2), (7, 24, -2), (7, 0, -2), (8, 40, -2), (8, 65552, -2)]
+    for i, v, rc in bad:
+        a = list(ok)
+        a[i] = v
+        assert L.moe_grouped_gemm_fp8(*a) == rc, (i, v)
+    a = list(ok)
+    a[6], a[8] = 4 << 20, 2048                              # gathered rows of 2^31 bytes
+    assert L.moe_grouped_gemm_fp8(*a) == -2
+    a[3], a[6], a[8] = 32, 1 << 27, 16                       # slot / k would not be exact
+    assert L.moe_grouped_gemm_fp8(*a) == -2
+    assert L.moe_grouped_gemm_fp8(None, None, None, 0, None, 8, 0, 64, 64, None, None, None, None, None) == 0
+    # x, x_scale, row_to_slot, k, offsets, E, R, d, f, w_gu, gu_scale, w_down, down_scale, row_scale, h, h_scale, y
+    ok = [P, P, P, 4, P, 8, 400, 64, 64, P, P, P, P, P, P, P, P, None]
+    for i in (0, 1, 4, 9, 10, 11, 12, 14, 15, 16):
+        for v in (None, MIS):
+            if i == 4 and v is MIS:
+                continue
+            a = list(ok)
+            a[i] = v
+            assert L.moe_grouped_ffn_fwd_fp8(*a) == -1, (i, v)
+    for i, v, rc in [(3, 0, -2), (3, 3, -1), (5, 0, -2), (6, -1, -1), (7, 40, -2), (8, 40, -2)]:
+        a = list(ok)
+        a[i] = v
+        assert L.moe_grouped_ffn_fwd_fp8(*a) == rc, (i, v)
+    assert L.moe_grouped_ffn_fwd_fp8(*([None] * 3 + [0, None, 8, 0, 64, 64] + [None] * 9)) == 0
