@@ -17,12 +17,15 @@
 // groups' sums and the accumulator in fp32.  The cut is taken for its rate
 // (twice that of bf16): the values have 4 significant bits, and the error it
 // leaves, about 1e-4 of a result, is a tenth of the bf16 store's.
+#include <type_traits>
+
 #include "moe_internal.h"
 
 namespace moe {
 namespace {
 
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
 
 constexpr int kBlk = 128;                                   // elements of a scale block
 constexpr float kMaxE4m3 = 448.0f;
@@ -224,11 +227,13 @@ struct Fp8Args {
 
 #define LDS_AS __attribute__((address_space(3)))
 
-// Raw buffer resource over [base, base + bytes): loads at or past the byte
-// count return zeros.
+// Raw buffer resource over [base, base + bytes), uniform over the wave: loads
+// at or past the byte count return zeros.
 __device__ __forceinline__ u32x4_t make_rsrc(const void *base, uint32_t bytes) {
   const uint64_t a = reinterpret_cast<uint64_t>(base);
-  return u32x4_t{(uint32_t)a, (uint32_t)(a >> 32) & 0xffffu, bytes, 0x00020000u};
+  return u32x4_t{(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)a),
+                 (uint32_t)__builtin_amdgcn_readfirstlane((int)(a >> 32)) & 0xffffu,
+                 (uint32_t)__builtin_amdgcn_readfirstlane((int)bytes), 0x00020000u};
 }
 constexpr uint32_t kOOB = 0x80000000u;   // at or past every resource's byte count
 
@@ -241,6 +246,16 @@ __device__ __forceinline__ void dma16(u32x4_t rs, uint32_t lds, uint32_t voff) {
                : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(voff), "s"(rs)
                : "memory", "m0");
 }
+// The same with 4 bytes per lane (lane l at lds + 4 l).
+__device__ __forceinline__ void dma4(u32x4_t rs, uint32_t lds, uint32_t voff) {
+  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+               :
+               : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(voff), "s"(rs)
+               : "memory", "m0");
+}
+__device__ __forceinline__ uint32_t lds_addr(const void *p) {
+  return (uint32_t)(uintptr_t)((const LDS_AS void *)p);
+}
 // s_waitcnt vmcnt(N) lgkmcnt(0)
 template <int N>
 __device__ __forceinline__ void wait_vm() {
@@ -248,361 +263,717 @@ __device__ __forceinline__ void wait_vm() {
   __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | ((N >> 4) << 14));
 }
 
-// Rows of expert e inside [0, R], whatever the offsets hold.
-__device__ __forceinline__ void segment(const Fp8Args &g, int e, int &seg0, int &rows) {
-  const int64_t a = min(max((int64_t)g.offsets[e], (int64_t)0), g.slots);
-  const int64_t b = min(max((int64_t)g.offsets[e + 1], a), g.slots);
-  seg0 = (int)a;
-  rows = (int)(b - a);
+// h = silu(g) u in fp32, the quotient by the hardware reciprocal (1 ulp)
+__device__ __forceinline__ float swiglu(float g, float u) {
+  return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
 }
 
-// The tile of this block of threads: the wave scans the experts' tile counts
-// (64 per step).  Tiles are numbered expert, then output columns, then rows
-// (fastest), and the numbers are split into 8 contiguous chunks, one per XCD
-// (blocks go round the XCDs), so that the tiles in flight on an XCD share
-// their weight slab in its L2.  Returns false if there is none.
-template <int BQ>
-__device__ __forceinline__ bool find_tile(const Fp8Args &g, int lane, int &e, int &pt, int &q0,
-                                          int &seg0, int &rows) {
-  int total = 0;
-  for (int e0 = 0; e0 < g.E; e0 += 64) {
-    int s = 0, n = 0;
-    if (e0 + lane < g.E) segment(g, e0 + lane, s, n);
-    n = (n + BQ - 1) / BQ;
-    for (int m = 1; m < 64; m <<= 1) n += __shfl_xor(n, m, 64);
-    total += n;
-  }
-  // tiles fit 32 bits: the host bounds the grid
-  const int all = __builtin_amdgcn_readfirstlane(total) * g.PT;
-  const int chunk = (all + 7) >> 3;
-  const int slot = (int)(blockIdx.x >> 3);
-  const int id = (int)(blockIdx.x & 7) * chunk + slot;
-  if (slot >= chunk || id >= all) return false;
-  int base = 0;
-  for (int e0 = 0; e0 < g.E; e0 += 64) {
-    int s = 0, n = 0;
-    if (e0 + lane < g.E) segment(g, e0 + lane, s, n);
-    const int t = (n + BQ - 1) / BQ * g.PT;
-    int end = t;   // inclusive scan
-    for (int m = 1; m < 64; m <<= 1) {
-      const int o = __shfl_up(end, m, 64);
-      if (lane >= m) end += o;
-    }
-    const uint64_t hit = __ballot(base + end > id);
-    if (hit) {
-      const int l = __ffsll((unsigned long long)hit) - 1;
-      const int tl = __builtin_amdgcn_readlane(t, l);
-      const int at = id - base - (__builtin_amdgcn_readlane(end, l) - tl);
-      rows = __builtin_amdgcn_readlane(n, l);
-      seg0 = __builtin_amdgcn_readlane(s, l);
-      e = e0 + l;
-      const int qt = (rows + BQ - 1) / BQ;
-      pt = at / qt;
-      q0 = (at % qt) * BQ;
-      return true;
-    }
-    base += __builtin_amdgcn_readlane(end, 63);
-  }
-  return false;
-}
-
-// h = silu(g) u in fp32
-__device__ __forceinline__ float swiglu(float g, float u) { return g / (1.0f + __expf(-g)) * u; }
+// every LDS access of this wave is done
+__device__ __forceinline__ void wait_lgkm() { __builtin_amdgcn_s_waitcnt(15 | (7 << 4) | (3 << 14)); }
 
 constexpr int kScaleChunk = 64;   // K blocks whose scales are in LDS at a time
 
-template <bool GU, int BP, int BQ, int WP, int WQ, int NS>
-__global__ __launch_bounds__(WP *WQ * 64) void k_grouped_fp8(Fp8Args g) {
-  constexpr int NW = WP * WQ;
-  constexpr int FP = BP / WP / 16, FQ = BQ / WQ / 16;   // a wave's fragments
-  constexpr int TQ = BQ * 8, TP = BP * 8;               // 16-byte chunks of a stage
-  constexpr int NIP = TP / 64 / NW;                     // loads per wave and stage
-  constexpr int NIQ = (TQ / 64 + NW - 1) / NW;
-  constexpr int LOADS = NIP + NIQ;
-  static_assert(NIP * 64 * NW == TP, "the P tile splits evenly over the waves");
-  static_assert(!GU || (BP == 256 && FP % 2 == 0), "a gate/up tile holds one block of 128 h");
-  static_assert(FP >= 1 && FQ >= 1 && NS >= 2 && (NS - 2) * LOADS < 64, "shape");
-  constexpr int STAGE = (TP + TQ) * 16;                 // bytes
-  constexpr int PITCH = (GU ? FP * 8 : FP * 32) + 16;   // epilogue: bytes of a row of 16 FP columns
-  static_assert(NW * 16 * PITCH <= NS * STAGE, "the epilogue's slots reuse the stages");
-  // P scale rows of a tile: gate/up, one block of gate rows and the two
-  // blocks that the up rows can touch; else BP / 128 (at least one)
-  constexpr int PB = GU ? 3 : (BP + 127) / 128;
-  __shared__ u32x4_t smem[NS * (TP + TQ)];
-  __shared__ u32x4_t s_dummy[64];
-  __shared__ uint32_t s_qs[kScaleChunk / 4][BQ];
+// A tile: expert, output columns from tile number pt, rows q0 .. q0 + qvalid - 1
+// of the expert's segment, which starts at row seg0.
+struct Tile {
+  int e, pt, q0, seg0, qvalid;
+};
+
+// The direct loads of a tile's K stages.  Instruction i of a wave covers 8
+// rows x 128 bytes; a lane's byte offset is fixed for the tile and the
+// resource's base moves with the stage.  Chunks past K read nothing, and so
+// does every chunk of a stage past the last one: such a stage leaves zeros.
+template <bool GU, int BP, int BQ, int NW>
+struct Loads {
+  static constexpr int TP = BP * 8, TQ = BQ * 8;               // 16-byte chunks of a stage
+  static constexpr int NIP = TP / 64 / NW;                     // instructions per wave and stage
+  static constexpr int NIQ = (TQ / 64 + NW - 1) / NW;
+  static constexpr int LOADS = NIP + NIQ;
+  static constexpr uint32_t STAGE = (TP + TQ) * 16;            // bytes
+  // every wave issues the same number of loads; those past the Q tile read
+  // nothing and land behind the ring
+  static constexpr bool SPARE = NIQ * 64 * NW > TQ;
+  static_assert(NIP * 64 * NW == TP && (NIQ == 1 || NIQ % 2 == 0), "loads per wave");
+  static_assert(NIP % 2 == 0, "the chunk a lane loads depends on its place's parity alone");
+  uint32_t voffP[NIP], voffQ[NIQ];
+  uint32_t leftP[2], leftQ[NIQ == 1 ? 1 : 2];   // K minus the lane's chunk offset, by parity of i
+  uint32_t spare;        // byte behind the ring
+  const uint8_t *pbase, *qbase;
+  uint32_t pbytes, qbytes;
+  uint32_t ldsP, ldsQ;   // the wave's places in the ring's first stage
+  int wave, lane;
+
+  __device__ __forceinline__ void init(const Fp8Args &g, int wave_, int lane_, const void *smem,
+                                       uint32_t ring) {
+    wave = wave_;
+    lane = lane_;
+    ldsP = lds_addr(smem) + (uint32_t)wave * (NIP * 1024u);
+    ldsQ = lds_addr(smem) + TP * 16u + (uint32_t)wave * (NIQ * 1024u);
+    spare = lds_addr(smem) + ring;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) leftP[i] = (uint32_t)max(g.K - (int)chunk(NIP * wave + i), 0);
+#pragma unroll
+    for (int i = 0; i < (NIQ == 1 ? 1 : 2); ++i) leftQ[i] = (uint32_t)max(g.K - (int)chunk(NIQ * wave + i), 0);
+  }
+  // row and byte of the chunk that a lane loads with instruction q of an operand
+  __device__ __forceinline__ int row(int q) const { return 8 * q + (lane >> 3); }
+  __device__ __forceinline__ uint32_t chunk(int q) const {
+    return (uint32_t)((lane & 7) ^ ((row(q) >> 1) & 7)) * 16u;
+  }
+  // src(r): the row of a (from qbase) that holds row r of the tile, or -1
+  template <typename Src>
+  __device__ __forceinline__ void tile(const Fp8Args &g, const Tile &t, Src src) {
+    // P: rows p0 .. of the expert; gate/up: the second half of the tile from row N + p0
+    const int K = g.K;
+    const int p0 = t.pt * (GU ? BP / 2 : BP);
+    const bool second = GU && wave * NIP * 8 >= BP / 2;
+    const int shift = second ? BP / 2 : 0;
+    const int64_t nmat = GU ? 2 * (int64_t)g.N : g.N;
+    pbase = g.b + (t.e * nmat + p0 + (second ? g.N : 0)) * K;
+    pbytes = (uint32_t)min(g.N - p0, GU ? BP / 2 : BP) * (uint32_t)K;
+#pragma unroll
+    for (int i = 0; i < NIP; ++i)
+      voffP[i] = (uint32_t)(row(NIP * wave + i) - shift) * (uint32_t)K + chunk(NIP * wave + i);
+    const bool gathered = g.row_to_slot != nullptr;
+    qbase = gathered ? g.a : g.a + ((int64_t)t.seg0 + t.q0) * K;
+    qbytes = gathered ? (uint32_t)(g.a_rows * K) : (uint32_t)t.qvalid * (uint32_t)K;
+#pragma unroll
+    for (int i = 0; i < NIQ; ++i) {
+      const int q = NIQ * wave + i;
+      const int r = SPARE && q * 8 >= BQ ? -1 : src(row(q));
+      voffQ[i] = r >= 0 ? (uint32_t)r * (uint32_t)K + chunk(q) : kOOB;
+    }
+  }
+  // one(i): instruction i of the stage at byte k0 of the rows, into the place
+  // of the ring at `buf`
+  __device__ __forceinline__ void one(int i, uint32_t k0, uint32_t buf) const {
+    const bool isp = i < NIP;
+    const int j = isp ? i : i - NIP;
+    const uint32_t bytes = isp ? pbytes : qbytes;
+    const u32x4_t rs = make_rsrc((isp ? pbase : qbase) + k0, max(bytes, k0) - k0);
+    const uint32_t to = (isp ? ldsP : ldsQ) + buf + (uint32_t)j * 1024u;
+    dma16(rs, SPARE && !isp && wave * 8 >= BQ ? spare : to,
+          k0 < (isp ? leftP[j & 1] : leftQ[NIQ == 1 ? 0 : j & 1]) ? (isp ? voffP[isp ? j : 0] : voffQ[isp ? 0 : j]) : kOOB);
+  }
+  __device__ __forceinline__ void issue(uint32_t k0, uint32_t buf) const {
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) one(i, k0, buf);
+  }
+};
+
+// Scale row of row r of the tile: gate/up, 0 for the gate rows (one block)
+// and 1, 2 for the two blocks that the up rows can touch; else one per 128.
+template <bool GU, int BP>
+__device__ __forceinline__ int p_block(const Fp8Args &g, int p0, int r) {
+  if (!GU) return r / kBlk;
+  return r < BP / 2 ? 0 : 1 + (g.N + p0 + r - BP / 2) / kBlk - (g.N + p0) / kBlk;
+}
+
+// 32 bytes of a fragment: chunks at `at` and at `at` with the bits `other` flipped.
+__device__ __forceinline__ i32x8_t frag(const LDS_AS char *lds, uint32_t at, uint32_t other) {
+  const u32x4_t lo = *reinterpret_cast<const LDS_AS u32x4_t *>(lds + at);
+  const u32x4_t hi = *reinterpret_cast<const LDS_AS u32x4_t *>(lds + (at ^ other));
+  return i32x8_t{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3],
+                 (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+}
+
+// Many rows: tiles of 256 x 256, 8 waves of 128 x 64 (4 x 2 fragments of
+// 32 x 32, MFMA 32x32x64: two steps per stage).  Persistent: one block of
+// threads per CU walks its tiles.
+//
+// A wave's K steps are pipelined: while the MFMAs of a step run, the next
+// step's fragments come from LDS, the Q fragments into the other register
+// set, a P fragment into its own registers once its MFMAs are issued.  The
+// barrier that publishes a stage stands before the last step of the stage
+// before it, whose fragments are all in registers then, so that its place in
+// the ring takes the loads of the stage after the published one; they go out
+// between the MFMAs.  After a tile's last stage the next tile's first stage
+// and scales are loaded while the epilogue runs, which uses the ring's other
+// place.
+template <bool GU>
+__global__ __launch_bounds__(512, 2) void k_grouped_fp8_wide(Fp8Args g) {
+  constexpr int BP = 256, BQ = 256, WP = 2, NW = 8, NS = 2, FP = 4, FQ = 2;
+  using L = Loads<GU, BP, BQ, NW>;
+  __shared__ u32x4_t smem[NS * (L::TP + L::TQ)];
+  __shared__ uint32_t s_qs[kScaleChunk / 4][BQ];   // scales of a chunk of K blocks, four to a dword
   __shared__ uint32_t s_ps[kScaleChunk / 4][4];
+  __shared__ int s_slot[BQ];                        // gathered rows: the next tile's slots
   __shared__ float s_amax[GU ? WP : 1][GU ? BQ : 1];
+  __shared__ int s_off[kMaxExperts + 1], s_ts[kMaxExperts + 1];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wp = wave % WP, wq = wave / WP;
-  int e, pt, q0, seg0, rows;
-  if (!find_tile<BQ>(g, lane, e, pt, q0, seg0, rows)) return;
-  const int K = g.K, N = g.N, cols = scale_cols(K), nk = scale_blocks(K);
-  const int p0 = pt * (GU ? BP / 2 : BP);
-  const int64_t nmat = GU ? 2 * (int64_t)N : N;         // rows of an expert's weights
-
-  // ---- row offsets of this wave's loads
-  uint32_t voffP[NIP], voffQ[NIQ];
-  const u32x4_t zero_rs = make_rsrc(g.offsets, 0);
-  // P: rows 0 .. BP-1 of the tile; gate/up: the second half from row N + p0
-  const bool second = GU && wave * NIP * 8 >= BP / 2;
-  const int prow_shift = second ? BP / 2 : 0;
-  const int pvalid = min(N - p0, GU ? BP / 2 : BP);
-  const uint8_t *pbase = g.b + (e * nmat + p0 + (second ? N : 0)) * K;
-#pragma unroll
-  for (int i = 0; i < NIP; ++i) {
-    const int row = 8 * (wave * NIP + i) + (lane >> 3);
-    const int ch = (lane & 7) ^ ((row >> 1) & 7);
-    voffP[i] = (uint32_t)(row - prow_shift) * (uint32_t)K + (uint32_t)ch * 16u;
-  }
-  const int qvalid = min(rows - q0, BQ);
+  const int N = g.N, nk = scale_blocks(g.K), cols = scale_cols(g.K);
   const bool gathered = g.row_to_slot != nullptr;
-  const uint8_t *qbase = gathered ? g.a : g.a + ((int64_t)seg0 + q0) * K;
-  const uint32_t qbytes = gathered ? (uint32_t)(g.a_rows * K) : (uint32_t)qvalid * (uint32_t)K;
-  // row of a that holds row q of the tile; -1 past the segment
-  auto source_row = [&](int q) -> int {
-    if (q >= qvalid) return -1;
-    if (!gathered) return q;
-    const uint32_t slot = (uint32_t)g.row_to_slot[(int64_t)seg0 + q0 + q];
-    return slot < (uint64_t)g.slots ? (int)(((uint64_t)slot * g.kmagic) >> 32) : -1;
-  };
+
+  // ---- tiles.  Numbered expert, then output columns, then rows (fastest),
+  // split into 8 contiguous chunks, one per XCD (blocks go round the XCDs):
+  // the tiles in flight on an XCD share their weight slab in its L2.
+  for (int i = tid; i <= g.E; i += NW * 64)
+    s_off[i] = (int)min(max((int64_t)g.offsets[i], (int64_t)0), g.slots);
+  __syncthreads();
+  if (wave == 0) {
+    int base = 0;
+    for (int e0 = 0; e0 < g.E; e0 += 64) {
+      const int e = e0 + lane;
+      int n = e < g.E ? (max(s_off[e + 1] - s_off[e], 0) + BQ - 1) / BQ * g.PT : 0;
 #pragma unroll
-  for (int i = 0; i < NIQ; ++i) {
-    const int row = 8 * (wave * NIQ + i) + (lane >> 3);
-    const int ch = (lane & 7) ^ ((row >> 1) & 7);
-    const int src = row < BQ ? source_row(row) : -1;
-    voffQ[i] = src >= 0 ? (uint32_t)src * (uint32_t)K + (uint32_t)ch * 16u : kOOB;
+      for (int m = 1; m < 64; m <<= 1) {
+        const int o = __shfl_up(n, m, 64);
+        if (lane >= m) n += o;
+      }
+      if (e < g.E) s_ts[e + 1] = base + n;
+      base += __builtin_amdgcn_readlane(n, 63);
+    }
+    if (lane == 0) s_ts[0] = 0;
   }
-
-  // Loads of K stage n into its place of the ring; past the last stage they
-  // read nothing into the spare slot (the count of loads per stage stays).
-  const uint32_t lds0 = (uint32_t)(uintptr_t)((const LDS_AS void *)smem);
-  const uint32_t dummy = (uint32_t)(uintptr_t)((const LDS_AS void *)s_dummy);
-  auto issue = [&](int n) {
-    const bool live = n < nk;
-    const uint32_t k0 = (uint32_t)n * 128u;
-    const u32x4_t rp = live ? make_rsrc(pbase + k0, (uint32_t)pvalid * (uint32_t)K - k0) : zero_rs;
-    const u32x4_t rq = live ? make_rsrc(qbase + k0, qbytes - k0) : zero_rs;
-    const uint32_t st = lds0 + (uint32_t)(n % NS) * STAGE;
-    const bool tail = k0 + 128u > (uint32_t)K;
-#pragma unroll
-    for (int i = 0; i < NIP; ++i) {
-      const int row = 8 * (wave * NIP + i) + (lane >> 3);
-      const uint32_t ch = (uint32_t)((lane & 7) ^ ((row >> 1) & 7));
-      const uint32_t off = tail && k0 + ch * 16u >= (uint32_t)K ? kOOB : voffP[i];
-      dma16(rp, live ? st + (uint32_t)(wave * NIP + i) * 1024u : dummy, off);
-    }
-#pragma unroll
-    for (int i = 0; i < NIQ; ++i) {
-      const int row = 8 * (wave * NIQ + i) + (lane >> 3);
-      const uint32_t ch = (uint32_t)((lane & 7) ^ ((row >> 1) & 7));
-      const uint32_t off = tail && k0 + ch * 16u >= (uint32_t)K ? kOOB : voffQ[i];
-      const bool in = live && (wave * NIQ + i) * 8 < BQ;
-      dma16(in ? rq : zero_rs, in ? st + TP * 16u + (uint32_t)(wave * NIQ + i) * 1024u : dummy, off);
+  __syncthreads();
+  const int total = __builtin_amdgcn_readfirstlane(s_ts[g.E]);
+  const int per = (int)(gridDim.x >> 3), chunk = (total + 7) >> 3;
+  const int cend = min(total, ((int)(blockIdx.x & 7) + 1) * chunk);
+  int id = (int)(blockIdx.x & 7) * chunk + (int)(blockIdx.x >> 3);
+  if (id >= cend) return;
+  auto decode = [&](int at) -> Tile {
+    for (int e0 = 0;; e0 += 64) {
+      const uint64_t hit = __ballot(e0 + lane < g.E && s_ts[min(e0 + lane, g.E - 1) + 1] > at);
+      if (hit) {
+        Tile t;
+        t.e = __builtin_amdgcn_readfirstlane(e0 + __ffsll((unsigned long long)hit) - 1);
+        t.seg0 = __builtin_amdgcn_readfirstlane(s_off[t.e]);
+        const int rows = __builtin_amdgcn_readfirstlane(s_off[t.e + 1]) - t.seg0;
+        const int qt = (rows + BQ - 1) / BQ;
+        const int in = at - __builtin_amdgcn_readfirstlane(s_ts[t.e]);
+        t.pt = in / qt;
+        t.q0 = (in % qt) * BQ;
+        t.qvalid = min(rows - t.q0, BQ);
+        return t;
+      }
     }
   };
-#pragma unroll
-  for (int n = 0; n < NS - 1; ++n) issue(n);
 
-  // ---- scales of kScaleChunk K blocks from block kc, as dwords of four
-  const int mbs = scale_blocks((int)nmat);
-  auto load_scales = [&](int kc) {
+  // ---- loads of a tile: its slots, its scales of a chunk of K blocks
+  L ld;
+  ld.init(g, wave, lane, smem, 0);
+  auto load_slots = [&](const Tile &t) {
+    if (wave < BQ / 64)
+      dma4(make_rsrc(g.row_to_slot + t.seg0 + t.q0, (uint32_t)t.qvalid * 4u),
+           lds_addr(s_slot + wave * 64), (uint32_t)(wave * 64 + lane) * 4u);
+  };
+  uint32_t sc_off = 0;   // of row 64 (wave % 4) + lane in the scale rows
+  auto set_tile = [&](const Tile &t) {
+    int ln = lane;   // taken anew, as in the epilogue
+    asm volatile("" : "+v"(ln));
+    ld.lane = ln;
+    auto src = [&](int r) -> int {   // row of a, -1 past the segment or for no token
+      if (r >= t.qvalid) return -1;
+      if (!gathered) return r;
+      const uint32_t slot = (uint32_t)s_slot[r];
+      return slot < (uint64_t)g.slots ? (int)(((uint64_t)slot * g.kmagic) >> 32) : -1;
+    };
+    ld.tile(g, t, src);
+    const int r = src((wave & 3) * 64 + ln);
+    sc_off = r >= 0 ? (uint32_t)r * (uint32_t)cols : kOOB;
+  };
+  auto load_scales = [&](const Tile &t, int kc) {
     const int nd = min(kScaleChunk, cols - kc) >> 2;
-    for (int i = tid; i < nd * BQ; i += NW * 64) {
-      const int q = i % BQ, w = i / BQ;
-      const int src = source_row(q);
-      const int64_t r = gathered ? src : (int64_t)seg0 + q0 + src;
-      s_qs[w][q] = src >= 0 ? *reinterpret_cast<const uint32_t *>(g.a_scale + r * cols + kc + 4 * w)
-                            : 0x7f7f7f7fu;
-    }
-    for (int i = tid; i < nd * PB; i += NW * 64) {
-      const int b = i % PB, w = i / PB;
+    const u32x4_t rs =
+        gathered ? make_rsrc(g.a_scale, (uint32_t)(g.a_rows * cols))
+                 : make_rsrc(g.a_scale + ((int64_t)t.seg0 + t.q0) * cols, (uint32_t)(t.qvalid * cols));
+    for (int w = wave >> 2; w < nd; w += 2)
+      dma4(rs, lds_addr(&s_qs[w][(wave & 3) * 64]), sc_off + (uint32_t)(kc + 4 * w));
+    if (wave == 0) {   // lane 4 w + b: dword w of scale row b
+      const int p0 = t.pt * (GU ? BP / 2 : BP);
+      const int mbs = scale_blocks((GU ? 2 : 1) * N);
+      const int b = lane & 3, w = lane >> 2;
       const int first = GU && b > 0 ? (N + p0) / kBlk + b - 1 : p0 / kBlk + b;
-      s_ps[w][b] = first < mbs ? *reinterpret_cast<const uint32_t *>(
-                                     g.b_scale + ((int64_t)e * mbs + first) * cols + kc + 4 * w)
-                               : 0x7f7f7f7fu;
+      const bool in = first < mbs && w < nd;
+      dma4(make_rsrc(g.b_scale + (int64_t)t.e * mbs * cols, (uint32_t)(mbs * cols)),
+           lds_addr(s_ps), in ? (uint32_t)(first * cols + kc + 4 * w) : kOOB);
     }
   };
-  load_scales(0);
 
   // ---- fragments
-  int prow[FP];   // first row of fragment i in the tile
+  const int lr = lane & 31, lg = lane >> 5;
+  int prow[FP];   // first row in the tile; gate/up: fragments 0, 1 gate, 2, 3 up
 #pragma unroll
   for (int i = 0; i < FP; ++i)
-    prow[i] = GU ? (i < FP / 2 ? 0 : BP / 2) + wp * (BP / 2 / WP) + 16 * (i % (FP / 2))
-                 : wp * (BP / WP) + 16 * i;
-  const int qrow0 = wq * (BQ / WQ);
-  // which of the PB scale rows fragment i takes (a fragment of 16 rows never
-  // straddles two blocks: N is a multiple of 16)
-  int pblk[FP];
-#pragma unroll
-  for (int i = 0; i < FP; ++i) {
-    if (!GU) pblk[i] = prow[i] / kBlk;
-    else if (i < FP / 2) pblk[i] = 0;
-    else pblk[i] = 1 + (N + p0 + prow[i] - BP / 2) / kBlk - (N + p0) / kBlk;
-  }
-  f32x4_t acc[FP][FQ];
-#pragma unroll
-  for (int i = 0; i < FP; ++i)
-#pragma unroll
-    for (int j = 0; j < FQ; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  const int lrow = lane & 15, lg = lane >> 4;
-  const uint32_t lane_off = (uint32_t)lrow * 128u + (uint32_t)((lg ^ ((lrow >> 1) & 7)) * 16);
+    prow[i] = GU ? (i >> 1) * (BP / 2) + wp * 64 + 32 * (i & 1) : wp * 128 + 32 * i;
+  // Q fragment j: rows 32 wq + 128 j, so that a tile's last rows are spread
+  // over the SIMDs
+  const int qrow0 = wq * 32;
   const LDS_AS char *lds = (const LDS_AS char *)smem;
-  auto frag = [&](uint32_t at) -> i32x8_t {
-    const u32x4_t lo = *reinterpret_cast<const LDS_AS u32x4_t *>(lds + at);
-    const u32x4_t hi = *reinterpret_cast<const LDS_AS u32x4_t *>(lds + (at ^ 64u));
-    return i32x8_t{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3],
-                   (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
-  };
-  const int nlive = min(FQ, max(0, (qvalid - qrow0 + 15) >> 4));   // Q fragments with rows
-
-  uint32_t sp[FP], sq[FQ];
+  // lane's first chunk of step 0: row lr, chunk lg; step 1: chunk bit 2, the
+  // fragment's second chunk: bit 1
+  const uint32_t at0 = (uint32_t)lr * 128u + (uint32_t)((lg ^ ((lr >> 1) & 7)) * 16);
+  Tile t = decode(id);
+  if (gathered) load_slots(t);
+  wait_vm<0>();
+  __syncthreads();
+  set_tile(t);
+  ld.issue(0, 0);
+  load_scales(t, 0);
+  wait_vm<0>();
+  for (;;) {
+    const int next = id + per;
+    const bool more = next < cend;
+    Tile tn = t;
+    if (more) tn = decode(next);
+    f32x16_t acc[FP][FQ];
 #pragma unroll
-  for (int i = 0; i < FP; ++i) sp[i] = 0;
+    for (int i = 0; i < FP; ++i)
 #pragma unroll
-  for (int j = 0; j < FQ; ++j) sq[j] = 0;
-  for (int n = 0; n < nk; ++n) {
-    if (n > 0 && n % kScaleChunk == 0) {
-      __syncthreads();
-      load_scales(n);
-    }
-    wait_vm<(NS - 2) * LOADS>();
-    __syncthreads();   // stage n (and the scales) are in LDS; stage n - 1 is read
+      for (int j = 0; j < FQ; ++j)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+    const int p0 = t.pt * (GU ? BP / 2 : BP);
+    int pblk[FP];
+#pragma unroll
+    for (int i = 0; i < FP; ++i) pblk[i] = p_block<GU, BP>(g, p0, prow[i] + lr);
+    // every wave's loads of stage 0 and the scales have landed (it waited for
+    // them), and every wave is done with the epilogue's slots
+    wait_lgkm();
+    __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    issue(n + NS - 1);
-    const int kc = n % kScaleChunk;
-    if ((kc & 3) == 0) {
+    if (more && gathered) load_slots(tn);
+    ld.issue(128, L::STAGE);
+
+    i32x8_t pf[FP], qf[2][FQ];
+    auto read_p = [&](int i, uint32_t at) { pf[i] = frag(lds + prow[i] * 128, at, 32u); };
+    auto read_q = [&](int set, uint32_t at) {
 #pragma unroll
-      for (int i = 0; i < FP; ++i) sp[i] = s_ps[kc >> 2][pblk[i]];
+      for (int j = 0; j < FQ; ++j) qf[set][j] = frag(lds + L::TP * 16 + (qrow0 + 128 * j) * 128, at, 32u);
+    };
+    // scales: of the stage at hand in the lowest byte, of the next ones above it
+    uint32_t sp[FP], sq[FQ], sp4[FP], sq4[FQ];
+    auto scales = [&](int n) {
+      const int w = ((unsigned)n % kScaleChunk) >> 2;
 #pragma unroll
-      for (int j = 0; j < FQ; ++j) sq[j] = s_qs[kc >> 2][qrow0 + 16 * j + lrow];
+      for (int i = 0; i < FP; ++i) sp4[i] = s_ps[w][pblk[i]];
+#pragma unroll
+      for (int j = 0; j < FQ; ++j) sq4[j] = s_qs[w][qrow0 + 128 * j + lr];
+    };
+    read_q(0, at0);
+#pragma unroll
+    for (int i = 0; i < FP; ++i) read_p(i, at0);
+    scales(0);
+#pragma unroll
+    for (int i = 0; i < FP; ++i) sp[i] = sp4[i];
+#pragma unroll
+    for (int j = 0; j < FQ; ++j) sq[j] = sq4[j];
+    // NL: the wave's Q fragments that hold rows
+    auto run = [&](auto nl) {
+      constexpr int NL = decltype(nl)::value;
+      uint32_t at = at0, k0 = 256;   // stage n's place; byte of stage n + 2
+      for (int n = 0;;) {
+        const int end = min(nk, (n / kScaleChunk + 1) * kScaleChunk);
+        // (no branch in the body: the compiler would move MFMAs over it)
+        for (; n < end; ++n) {
+          // step 0, and the reads of step 1's fragments
+          read_q(1, at ^ 64u);
+#pragma unroll
+          for (int i = 0; i < FP; ++i) {
+#pragma unroll
+            for (int j = 0; j < NL; ++j)
+              acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                  pf[i], qf[0][j], acc[i][j], 0, 0, 0, (int)sp[i], 0, (int)sq[j]);
+            __builtin_amdgcn_sched_barrier(0);
+            read_p(i, at ^ 64u);
+          }
+          // stage n + 1 has landed everywhere, and stage n is read (its last
+          // fragments are in registers): its place is free
+          asm volatile("" ::: "memory");
+          __builtin_amdgcn_sched_barrier(0);
+          wait_vm<0>();
+          __builtin_amdgcn_s_barrier();
+          asm volatile("" ::: "memory");
+          __builtin_amdgcn_sched_barrier(0);
+          // step 1, the reads of stage n + 1's step 0 and the loads of stage n + 2
+          const uint32_t buf = n & 1 ? L::STAGE : 0u;
+          at ^= L::STAGE;
+          scales(n + 1);
+          read_q(0, at);
+#pragma unroll
+          for (int i = 0; i < FP; ++i) {
+#pragma unroll
+            for (int j = 0; j < FQ; ++j) {
+              if (j < NL)
+                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                    pf[i], qf[1][j], acc[i][j], 0, 0, 0, (int)sp[i], 0, (int)sq[j]);
+              ld.one(2 * i + j, k0, buf);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            read_p(i, at);
+          }
+          k0 += 128;
+          const bool fresh = ((n + 1) & 3) == 0;
+#pragma unroll
+          for (int i = 0; i < FP; ++i) sp[i] = fresh ? sp4[i] : sp[i] >> 8;
+#pragma unroll
+          for (int j = 0; j < FQ; ++j) sq[j] = fresh ? sq4[j] : sq[j] >> 8;
+        }
+        if (n >= nk) break;
+        wait_lgkm();
+        __builtin_amdgcn_s_barrier();
+        load_scales(t, n);
+        wait_vm<0>();
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        scales(n);
+#pragma unroll
+        for (int i = 0; i < FP; ++i) sp[i] = sp4[i];
+#pragma unroll
+        for (int j = 0; j < FQ; ++j) sq[j] = sq4[j];
+      }
+    };
+    const int nlive = (t.qvalid > qrow0) + (t.qvalid > qrow0 + 128);
+    if (nlive == 2) run(std::integral_constant<int, 2>{});
+    else if (nlive == 1) run(std::integral_constant<int, 1>{});
+    else run(std::integral_constant<int, 0>{});
+
+    // every wave is done with the ring (the empty stages' zeros too) and the scales
+    asm volatile("" ::: "memory");
+    wait_vm<0>();
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    if (more) {
+      set_tile(tn);
+      ld.issue(0, 0);
+      load_scales(tn, 0);
     }
-    const uint32_t st = (uint32_t)(n % NS) * STAGE;
-    i32x8_t pf[FP];
+
+    // Epilogue.  Lane holds D[8 (v / 4) + 4 (lane / 32) + v % 4][lane % 32] of each fragment;
+    // the results go through the wave's own slot in the ring's second place,
+    // so that the stores are 16 bytes per lane.
+    // (The lane number is taken anew: addresses kept over the main loop would
+    // not fit its registers.)
+    int ln = lane;
+    asm volatile("" : "+v"(ln));
+    const int er = ln & 31, eg = ln >> 5;
+    const int64_t r0 = (int64_t)t.seg0 + t.q0;
+    LDS_AS char *const slot = (LDS_AS char *)smem + L::STAGE + wave * (L::STAGE / NW);
+    if constexpr (GU) {
+      constexpr int PITCH = 64 + 16;
 #pragma unroll
-    for (int i = 0; i < FP; ++i) pf[i] = frag(st + (uint32_t)prow[i] * 128u + lane_off);
+      for (int j = 0; j < FQ; ++j) {
+        float m = 0.0f;
+        if (j < nlive) {
 #pragma unroll
-    for (int j = 0; j < FQ; ++j) {
-      if (j < nlive) {
-        const i32x8_t qf = frag(st + TP * 16u + (uint32_t)(qrow0 + 16 * j) * 128u + lane_off);
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) {
+              const float h = swiglu(acc[i][j][v], acc[i + 2][j][v]);
+              acc[i][j][v] = h;
+              m = fmaxf(m, fabsf(h));   // a NaN is passed over
+            }
+          // an infinity is passed over too, and turned to NaN: the rare case
+          // costs a second pass over the values
+          if (__any(m > 3.402823466e38f)) {
+            m = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int v = 0; v < 16; ++v) {
+                m = fmaxf(m, finite_abs(acc[i][j][v]));
+                acc[i][j][v] = scaled(acc[i][j][v], 1.0f);
+              }
+          }
+          m = fmaxf(m, __shfl_xor(m, 32, 64));
+        }
+        if (ln < 32) s_amax[wp][qrow0 + 128 * j + ln] = m;
+      }
+      wait_lgkm();
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      const int hcols = scale_cols(N);
+#pragma unroll
+      for (int j = 0; j < FQ; ++j) {
+        if (j >= nlive) continue;
+        const int q = qrow0 + 128 * j + er;
+        const uint32_t byte = scale_byte(fmaxf(s_amax[0][q], s_amax[WP - 1][q]));
+        const float inv = inv_scale(byte);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int v = 0; v < 16; v += 4)
+            *reinterpret_cast<LDS_AS uint32_t *>(slot + er * PITCH + 32 * i + 2 * v + 4 * eg) =
+                pack_e4m3x4(acc[i][j][v] * inv, acc[i][j][v + 1] * inv, acc[i][j][v + 2] * inv,
+                            acc[i][j][v + 3] * inv);
+        if (j == 0) wait_vm<0>();   // the next tile's loads; before the stores, which need not be waited for
+        if (wp == 0 && eg == 0 && q < t.qvalid) {
+          g.h_scale[(r0 + q) * hcols + t.pt] = (uint8_t)byte;
+          if (t.pt == g.PT - 1)
+            for (int b = t.pt + 1; b < hcols; ++b) g.h_scale[(r0 + q) * hcols + b] = 127;
+        }
+#pragma unroll
+        for (int rr = 0; rr < 32; rr += 16) {   // 4 lanes x 16 bytes per row
+          const int row = rr + (ln >> 2), ch = ln & 3;
+          const u32x4_t val = *reinterpret_cast<const LDS_AS u32x4_t *>(slot + row * PITCH + 16 * ch);
+          const int qq = qrow0 + 128 * j + row, n = p0 + wp * 64 + 16 * ch;
+          if (qq < t.qvalid && n < N) *reinterpret_cast<u32x4_t *>(g.h + (r0 + qq) * N + n) = val;
+        }
+      }
+    } else {
+      // rows of 256 bytes, chunk c of 16 bytes at place c ^ (row & 15)
+#pragma unroll
+      for (int j = 0; j < FQ; ++j) {
+        if (j >= nlive) continue;
+        const int q = qrow0 + 128 * j + er;
+        const float w = g.row_scale && q < t.qvalid ? g.row_scale[r0 + q] : 1.0f;
 #pragma unroll
         for (int i = 0; i < FP; ++i)
-          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-              pf[i], qf, acc[i][j], 0, 0, 0, (int)sp[i], 0, (int)sq[j]);
+#pragma unroll
+          for (int v = 0; v < 16; v += 4)
+            *reinterpret_cast<LDS_AS u32x2_t *>(slot + er * 256 + ((4 * i + v / 4) ^ (er & 15)) * 16 + 8 * eg) =
+                u32x2_t{pack_bf16x2(w * acc[i][j][v], w * acc[i][j][v + 1]),
+                        pack_bf16x2(w * acc[i][j][v + 2], w * acc[i][j][v + 3])};
+        if (j == 0) wait_vm<0>();   // the next tile's loads; before the stores, which need not be waited for
+#pragma unroll
+        for (int rr = 0; rr < 32; rr += 4) {   // 16 lanes x 16 bytes per row
+          const int row = rr + (ln >> 4), ch = ln & 15;
+          const u32x4_t val =
+              *reinterpret_cast<const LDS_AS u32x4_t *>(slot + row * 256 + (ch ^ (row & 15)) * 16);
+          const int qq = qrow0 + 128 * j + row, n = p0 + wp * 128 + 8 * ch;
+          if (qq < t.qvalid && n < N) *reinterpret_cast<u32x4_t *>(g.c + (r0 + qq) * N + n) = val;
+        }
       }
     }
-#pragma unroll
-    for (int i = 0; i < FP; ++i) sp[i] >>= 8;
-#pragma unroll
-    for (int j = 0; j < FQ; ++j) sq[j] >>= 8;
+    if (nlive == 0) wait_vm<0>();
+    if (!more) break;
+    t = tn;
+    id = next;
   }
+}
 
-  // ---- epilogue: 16 rows x the wave's columns at a time through the wave's
-  // own LDS slot, so that the stores are 16 bytes per lane
-  wait_vm<0>();
-  __syncthreads();   // every wave is done with the stages, whose space the slots take
-  LDS_AS char *slot = (LDS_AS char *)smem + wave * 16 * PITCH;
-  if constexpr (GU) {
-    constexpr int FH = FP / 2;
-    // h in the gate accumulators, and the largest magnitude of each row
+// Few rows per expert: the weights' way from memory bounds.  A block of
+// threads takes 256 weight rows (gate/up: 128 gate and 128 up, one block of
+// h; else BP) against up to BQ rows of an expert at a time, over all of K,
+// with NS - 1 stages on their way, and walks on by BQ rows if the expert has
+// more.  8 waves side by side along the weight rows, 16 x 16 fragments (MFMA
+// 16x16x128, one per stage and fragment pair).
+template <bool GU, int BP, int BQ, int NS>
+__global__ __launch_bounds__(512) void k_grouped_fp8_few(Fp8Args g) {
+  constexpr int NW = 8, FP = BP / NW / 16, FQ = BQ / 16;
+  using L = Loads<GU, BP, BQ, NW>;
+  static_assert(!GU || BP == 256, "a gate/up tile holds one block of 128 h");
+  static_assert((NS - 2) * L::LOADS < 64, "vmcnt range");
+  __shared__ u32x4_t smem[NS * (L::TP + L::TQ) + 64];
+  __shared__ uint32_t s_qs[kScaleChunk / 4][64];
+  __shared__ uint32_t s_ps[kScaleChunk / 4][4];
+  __shared__ float s_amax[GU ? NW : 1][GU ? BQ : 1];
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int N = g.N, nk = scale_blocks(g.K), cols = scale_cols(g.K);
+  const bool gathered = g.row_to_slot != nullptr;
+
+  // the (blockIdx.y)-th expert that has rows
+  Tile t;
+  int rows = 0;
+  {
+    int want = (int)blockIdx.y;
+    t.e = -1;
+    for (int e0 = 0; e0 < g.E && t.e < 0; e0 += 64) {
+      int a = 0, n = 0;
+      if (e0 + lane < g.E) {
+        a = (int)min(max((int64_t)g.offsets[e0 + lane], (int64_t)0), g.slots);
+        n = (int)min(max((int64_t)g.offsets[e0 + lane + 1], (int64_t)0), g.slots) - a;
+      }
+      uint64_t full = __ballot(n > 0);
+      const int here = __popcll(full);
+      if (want >= here) {
+        want -= here;
+        continue;
+      }
+      for (; want > 0; --want) full &= full - 1;
+      const int l = __ffsll((unsigned long long)full) - 1;
+      t.e = e0 + l;
+      t.seg0 = __builtin_amdgcn_readlane(a, l);
+      rows = __builtin_amdgcn_readlane(n, l);
+    }
+    if (t.e < 0) return;
+    t.e = __builtin_amdgcn_readfirstlane(t.e);
+  }
+  t.pt = (int)blockIdx.x;
+  const int p0 = t.pt * (GU ? BP / 2 : BP);
+  const int lr = lane & 15, lg = lane >> 4;
+  int prow[FP], pblk[FP];
 #pragma unroll
-    for (int j = 0; j < FQ; ++j) {
-      float m = 0.0f;
+  for (int i = 0; i < FP; ++i) {
+    prow[i] = GU ? i * (BP / 2) + 16 * wave : 16 * (FP * wave + i);
+    pblk[i] = p_block<GU, BP>(g, p0, prow[i]);   // 16 rows lie in one block: N is a multiple of 16
+  }
+  const LDS_AS char *lds = (const LDS_AS char *)smem;
+  const uint32_t at0 = (uint32_t)lr * 128u + (uint32_t)((lg ^ ((lr >> 1) & 7)) * 16);
+  L ld;
+  ld.init(g, wave, lane, smem, NS * L::STAGE);
+
+  for (t.q0 = 0; t.q0 < rows; t.q0 += BQ) {
+    t.qvalid = min(rows - t.q0, BQ);
+    auto src = [&](int r) -> int {   // row of a, -1 past the segment or for no token
+      if (r >= t.qvalid) return -1;
+      if (!gathered) return r;
+      const uint32_t slot = (uint32_t)g.row_to_slot[(int64_t)t.seg0 + t.q0 + r];
+      return slot < (uint64_t)g.slots ? (int)(((uint64_t)slot * g.kmagic) >> 32) : -1;
+    };
+    const int srow = src(lane);
+    ld.tile(g, t, src);
 #pragma unroll
-      for (int i = 0; i < FH; ++i)
+    for (int n = 0; n < NS - 1; ++n) ld.issue(128u * n, n * L::STAGE);
+    auto load_scales = [&](int kc) {   // as in the wide kernel; one row per lane
+      const int nd = min(kScaleChunk, cols - kc) >> 2;
+      const u32x4_t rs =
+          gathered ? make_rsrc(g.a_scale, (uint32_t)(g.a_rows * cols))
+                   : make_rsrc(g.a_scale + ((int64_t)t.seg0 + t.q0) * cols, (uint32_t)(t.qvalid * cols));
+      for (int w = wave; w < nd; w += NW)
+        dma4(rs, lds_addr(&s_qs[w][0]), srow >= 0 ? (uint32_t)srow * (uint32_t)cols + (uint32_t)(kc + 4 * w) : kOOB);
+      if (wave == 0) {
+        const int mbs = scale_blocks((GU ? 2 : 1) * N);
+        const int b = lane & 3, w = lane >> 2;
+        const int first = GU && b > 0 ? (N + p0) / kBlk + b - 1 : p0 / kBlk + b;
+        dma4(make_rsrc(g.b_scale + (int64_t)t.e * mbs * cols, (uint32_t)(mbs * cols)), lds_addr(s_ps),
+             first < mbs && w < nd ? (uint32_t)(first * cols + kc + 4 * w) : kOOB);
+      }
+    };
+    load_scales(0);
+    f32x4_t acc[FP][FQ];
+#pragma unroll
+    for (int i = 0; i < FP; ++i)
+#pragma unroll
+      for (int j = 0; j < FQ; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    wait_vm<0>();   // the scales, and with them the first stages
+    __builtin_amdgcn_s_barrier();
+    uint32_t buf = 0, last = (NS - 1) * L::STAGE;   // places of stage n and of stage n + NS - 1
+    const int nlive = (t.qvalid + 15) >> 4;
+    for (int n = 0; n < nk; ++n) {
+      if (n > 0 && n % kScaleChunk == 0) {
+        wait_lgkm();
+        __builtin_amdgcn_s_barrier();
+        load_scales(n);
+        wait_vm<0>();
+      }
+      // stage n has landed everywhere and stage n - 1 is read
+      asm volatile("" ::: "memory");
+      wait_vm<(NS - 2) * L::LOADS>();
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      ld.issue(128u * (n + NS - 1), last);
+      const int w = (n % kScaleChunk) >> 2, sh = (n & 3) * 8;
+      i32x8_t pf[FP];
+      uint32_t sp[FP];
+#pragma unroll
+      for (int i = 0; i < FP; ++i) {
+        pf[i] = frag(lds + prow[i] * 128, buf + at0, 64u);
+        sp[i] = s_ps[w][pblk[i]] >> sh;
+      }
+#pragma unroll
+      for (int j = 0; j < FQ; ++j) {
+        if (j < nlive) {
+          const i32x8_t qf = frag(lds + L::TP * 16 + 16 * j * 128, buf + at0, 64u);
+          const uint32_t sq = s_qs[w][16 * j + lr] >> sh;
+#pragma unroll
+          for (int i = 0; i < FP; ++i)
+            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                pf[i], qf, acc[i][j], 0, 0, 0, (int)sp[i], 0, (int)sq);
+        }
+      }
+      buf = buf == (NS - 1) * L::STAGE ? 0u : buf + L::STAGE;
+      last = last == (NS - 1) * L::STAGE ? 0u : last + L::STAGE;
+    }
+    asm volatile("" ::: "memory");
+    wait_vm<0>();
+    __builtin_amdgcn_s_barrier();   // every wave is done with the ring and the scales
+    asm volatile("" ::: "memory");
+
+    // Epilogue.  Lane holds D[4 lg + v][lr] of each fragment.
+    const int64_t r0 = (int64_t)t.seg0 + t.q0;
+    if constexpr (GU) {
+#pragma unroll
+      for (int j = 0; j < FQ; ++j) {
+        float m = 0.0f;
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
-          const float h = swiglu(acc[i][j][v], acc[i + FH][j][v]);
-          acc[i][j][v] = h;
-          m = fmaxf(m, finite_abs(h));
+          acc[0][j][v] = swiglu(acc[0][j][v], acc[1][j][v]);
+          m = fmaxf(m, finite_abs(acc[0][j][v]));
         }
-      m = fmaxf(m, __shfl_xor(m, 16, 64));
-      m = fmaxf(m, __shfl_xor(m, 32, 64));
-      if (lane < 16) s_amax[wp][qrow0 + 16 * j + lane] = m;
-    }
-    __syncthreads();
-    const int hcols = scale_cols(N);
-#pragma unroll
-    for (int j = 0; j < FQ; ++j) {
-      if (j >= nlive) continue;
-      const int q = qrow0 + 16 * j + lrow;
-      float m = 0.0f;
-#pragma unroll
-      for (int w = 0; w < WP; ++w) m = fmaxf(m, s_amax[w][q]);
-      const uint32_t byte = scale_byte(m);
-      const float inv = inv_scale(byte);
-      const int64_t r = (int64_t)seg0 + q0 + q;
-      if (wp == 0 && lg == 0 && q < qvalid) {
-        g.h_scale[r * hcols + pt] = (uint8_t)byte;
-        if (pt == g.PT - 1)
-          for (int b = pt + 1; b < hcols; ++b) g.h_scale[r * hcols + b] = 127;
+        m = fmaxf(m, __shfl_xor(m, 16, 64));
+        m = fmaxf(m, __shfl_xor(m, 32, 64));
+        if (lane < 16) s_amax[wave][16 * j + lane] = m;
       }
+      wait_lgkm();
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      const int hcols = scale_cols(N);
 #pragma unroll
-      for (int i = 0; i < FH; ++i)
-        *reinterpret_cast<LDS_AS uint32_t *>(slot + lrow * PITCH + 16 * i + 4 * lg) =
-            pack_e4m3x4(scaled(acc[i][j][0], inv), scaled(acc[i][j][1], inv),
-                        scaled(acc[i][j][2], inv), scaled(acc[i][j][3], inv));
-      constexpr int CPR = FH, RPI = 64 / CPR;   // 16-byte chunks per row, rows per step
+      for (int j = 0; j < FQ; ++j) {
+        const int q = 16 * j + lr;
+        float m = 0.0f;
 #pragma unroll
-      for (int rr = 0; rr < 16; rr += RPI) {
-        const int row = rr + lane / CPR, ch = lane % CPR;
-        if (row >= 16) continue;
-        const u32x4_t val = *reinterpret_cast<const LDS_AS u32x4_t *>(slot + row * PITCH + 16 * ch);
-        const int qq = qrow0 + 16 * j + row, n = p0 + wp * (BP / 2 / WP) + 16 * ch;
-        if (qq < qvalid && n < N)
-          *reinterpret_cast<u32x4_t *>(g.h + ((int64_t)seg0 + q0 + qq) * N + n) = val;
+        for (int i = 0; i < NW; ++i) m = fmaxf(m, s_amax[i][q]);
+        const uint32_t byte = scale_byte(m);
+        const float inv = inv_scale(byte);
+        if (q < t.qvalid) {
+          const int n = p0 + prow[0] + 4 * lg;
+          if (n < N)
+            *reinterpret_cast<uint32_t *>(g.h + (r0 + q) * N + n) =
+                pack_e4m3x4(scaled(acc[0][j][0], inv), scaled(acc[0][j][1], inv),
+                            scaled(acc[0][j][2], inv), scaled(acc[0][j][3], inv));
+          if (wave == 0 && lg == 0) {
+            g.h_scale[(r0 + q) * hcols + t.pt] = (uint8_t)byte;
+            if (t.pt == g.PT - 1)
+              for (int b = t.pt + 1; b < hcols; ++b) g.h_scale[(r0 + q) * hcols + b] = 127;
+          }
+        }
       }
-    }
-  } else {
+    } else {
 #pragma unroll
-    for (int j = 0; j < FQ; ++j) {
-      if (j >= nlive) continue;
-      const int q = qrow0 + 16 * j + lrow;
-      const float w = g.row_scale && q < qvalid ? g.row_scale[(int64_t)seg0 + q0 + q] : 1.0f;
+      for (int j = 0; j < FQ; ++j) {
+        const int q = 16 * j + lr;
+        if (q >= t.qvalid) continue;
+        const float w = g.row_scale ? g.row_scale[r0 + q] : 1.0f;
 #pragma unroll
-      for (int i = 0; i < FP; ++i)
-        *reinterpret_cast<LDS_AS u32x2_t *>(slot + lrow * PITCH + 32 * i + 8 * lg) =
-            u32x2_t{pack_bf16x2(w * acc[i][j][0], w * acc[i][j][1]),
-                    pack_bf16x2(w * acc[i][j][2], w * acc[i][j][3])};
-      constexpr int CPR = 2 * FP, RPI = 64 / CPR;
-#pragma unroll
-      for (int rr = 0; rr < 16; rr += RPI) {
-        const int row = rr + lane / CPR, ch = lane % CPR;
-        if (row >= 16) continue;
-        const u32x4_t val = *reinterpret_cast<const LDS_AS u32x4_t *>(slot + row * PITCH + 16 * ch);
-        const int qq = qrow0 + 16 * j + row, n = p0 + wp * (BP / WP) + 8 * ch;
-        if (qq < qvalid && n < N)
-          *reinterpret_cast<u32x4_t *>(g.c + ((int64_t)seg0 + q0 + qq) * N + n) = val;
+        for (int i = 0; i < FP; ++i) {
+          const int n = p0 + prow[i] + 4 * lg;
+          if (n < N)
+            *reinterpret_cast<u32x2_t *>(g.c + (r0 + q) * N + n) =
+                u32x2_t{pack_bf16x2(w * acc[i][j][0], w * acc[i][j][1]),
+                        pack_bf16x2(w * acc[i][j][2], w * acc[i][j][3])};
+        }
       }
     }
+    // the next rows' loads and scales must not pass this block's reads of s_amax
+    wait_lgkm();
+    __builtin_amdgcn_s_barrier();
   }
 }
 
-// Blocks for a product over R rows: every expert ends with a partial tile at
-// most, and no more experts have rows than there are rows.
-int64_t grid_blocks(int64_t R, int E, int BQ, int PT) {
-  const int64_t q = R / BQ + (E < R ? (int64_t)E : R);
-  return (q * PT + 7) / 8 * 8;
-}
-
-template <bool GU, int BP, int BQ, int WP, int WQ, int NS>
-int launch_product(const Fp8Args &args, const char *name, const char *fn, hipStream_t s) {
-  Fp8Args g = args;
-  const int per = GU ? BP / 2 : BP;
-  g.PT = (g.N + per - 1) / per;
-  const int64_t blocks = grid_blocks(g.slots, g.E, BQ, g.PT);
-  MOE_REQUIRE(blocks < ((int64_t)1 << 31), MOE_ERR_UNSUPPORTED, "%s: too many tiles", fn);
-  MOE_LAUNCH(name, s,
-             (k_grouped_fp8<GU, BP, BQ, WP, WQ, NS><<<(unsigned)blocks, WP * WQ * 64, 0, s>>>(g)));
-  return check_launch(fn);
-}
+// Rows per expert (on average, of those that can have rows) up to which the
+// few-rows kernel runs.  At d = f = 2880, 32 experts, gate/up + down: 105 + 58
+// us against the other's 128 + 82 at 8 rows, 111 + 65 against 133 + 85 at 32,
+// 154 + 91 against 145 + 93 at 64.
+constexpr int64_t kFewRows = 48;
+constexpr int kCUs = 256;   // persistent kernels: one block of threads per CU, a multiple of 8
 
 template <bool GU>
-int product(const Fp8Args &g, const char *name, const char *fn, hipStream_t s) {
-  return launch_product<GU, 256, 128, 4, 2, 2>(g, name, fn, s);
+int product(const Fp8Args &args, const char *name, const char *fn, hipStream_t s) {
+  Fp8Args g = args;
+  const int64_t active = g.E < g.slots ? (int64_t)g.E : g.slots;   // experts with rows, at most
+  if (g.slots <= kFewRows * active) {
+    constexpr int BP = GU ? 256 : 128;
+    const int per = 128;
+    g.PT = (g.N + per - 1) / per;
+    const dim3 grid((unsigned)g.PT, (unsigned)active);
+    MOE_LAUNCH(name, s, (k_grouped_fp8_few<GU, BP, 64, GU ? 3 : 5><<<grid, 512, 0, s>>>(g)));
+    return check_launch(fn);
+  }
+  const int per = GU ? 128 : 256;
+  g.PT = (g.N + per - 1) / per;
+  // tile numbers are 32-bit; an expert ends with a partial tile at most
+  const int64_t tiles = (g.slots / 256 + active) * g.PT;
+  MOE_REQUIRE(tiles < ((int64_t)1 << 30), MOE_ERR_UNSUPPORTED, "%s: too many tiles", fn);
+  const unsigned blocks = (unsigned)min((tiles + 7) / 8 * 8, (int64_t)kCUs);
+  MOE_LAUNCH(name, s, (k_grouped_fp8_wide<GU><<<blocks, 512, 0, s>>>(g)));
+  return check_launch(fn);
 }
 
 constexpr int kMaxDim = 1 << 16;
