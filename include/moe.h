@@ -493,7 +493,8 @@ int moe_route_scored(const float *logits, const float *sel_bias, int64_t T, int 
  *   softmax, plain (every e): -scale s_e m, and w_j g_j added at the selected.
  * d_logits: [T,E] (out, fully written); it can be given to
  * moe_router_logits_bwd and moe_permute_bwd_router.  score, renorm and scale
- * as in the forward call; logits, d_logits 16-byte aligned; the two must not
+ * as in the forward call; topk_idx distinct within a token (an id outside
+ * [0,E) gets nothing); logits, d_logits 16-byte aligned; the two must not
  * overlap.  A row whose weights are all 0 gets zeros.
  */
 int moe_route_scored_bwd(const float *logits, const int32_t *topk_idx, const float *topk_w,
