@@ -22,6 +22,16 @@ written by moe_permute for the dW_gu GEMM (its stored rows are the faster
 operand there) unless ``store_x_perm`` is False; then moe_permute writes only
 the maps and w_perm and the dW_gu GEMM gathers X too.
 
+With ``router`` (a ScoreRouter) moe_route_scored / moe_route_scored_bwd take
+the place of moe_route / moe_route_bwd: softmax or sigmoid scores over all
+experts, expert groups, weights renormalised or not.
+
+With ``fp8`` the experts are frozen 8-bit weights (quantize_experts()) and the
+block runs forward only: moe_quant_rows_fp8 over the T token rows, then
+moe_grouped_ffn_fwd_fp8, whose gate/up product reads the rows of a token where
+it loads them; past that call's limits (gather_fits_fp8()) the rows are
+permuted and quantised as R rows.
+
 With ``lora_rank`` set the experts are frozen and carry LoRA factors:
 moe_grouped_ffn_fwd_lora / moe_grouped_ffn_bwd_lora replace the grouped-FFN
 calls, and the backward forms the LoRA factor gradients instead of the expert
@@ -35,6 +45,7 @@ the dispatch and combine all-to-alls reduced to on-GPU row permutations.
 """
 from __future__ import annotations
 
+from dataclasses import dataclass
 from typing import Dict, Optional
 
 import torch
@@ -49,11 +60,75 @@ def gather_fits(T: int, d: int, k: int) -> bool:
     return T * d < (1 << 30) and T * k * k < (1 << 32)
 
 
+def gather_fits_fp8(T: int, d: int, k: int) -> bool:
+    """Whether moe_grouped_ffn_fwd_fp8 takes the token rows unpermuted: their
+    byte offsets are 31-bit and the slot -> token division is exact."""
+    return T * d < (1 << 31) and T * k * k < (1 << 32)
+
+
+@dataclass(frozen=True)
+class ScoreRouter:
+    """How moe_route_scored routes: see include/moe.h for each field."""
+    score: str = "softmax"       # or "sigmoid"
+    n_group: int = 1
+    topk_group: int = 1
+    group_top: int = 1
+    renorm: bool = True
+    scale: float = 1.0
+
+    def __post_init__(self):
+        if self.score not in ("softmax", "sigmoid"):
+            raise ValueError("score must be 'softmax' or 'sigmoid', not %r" % (self.score,))
+
+    @property
+    def code(self) -> int:
+        return abi.MOE_SCORE_SIGMOID if self.score == "sigmoid" else abi.MOE_SCORE_SOFTMAX
+
+    def forward(self, logits, sel_bias, k, topk_idx, topk_w, stream=None):
+        abi.moe_route_scored(logits, sel_bias, k, topk_idx, topk_w, score=self.code,
+                             n_group=self.n_group, topk_group=self.topk_group,
+                             group_top=self.group_top, renorm=self.renorm, scale=self.scale,
+                             stream=stream)
+
+    def backward(self, logits, topk_idx, topk_w, d_row_scale, slot_to_row, d_topk_w, d_logits,
+                 stream=None):
+        abi.moe_route_scored_bwd(logits, topk_idx, topk_w, d_row_scale, slot_to_row, d_topk_w,
+                                 d_logits, score=self.code, renorm=self.renorm, scale=self.scale,
+                                 stream=stream)
+
+
+def quantize_weights(w, transposed: bool = False, stream=None):
+    """8-bit weights of w [E,N,K]: (q, scale), with ``transposed`` (q, scale,
+    qt, scale_t), the last two for the product that forms the rows' gradient."""
+    E, N, K = w.shape
+    z = lambda *s, dt: torch.empty(*s, dtype=dt, device=w.device)
+    q8, u8 = torch.float8_e4m3fn, torch.uint8
+    q = z(E, N, K, dt=q8)
+    scale = z(E, (N + 127) // 128, abi.moe_fp8_scale_cols(K), dt=u8)
+    if not transposed:
+        abi.moe_quant_weights_fp8(w, q, scale, stream=stream)
+        return q, scale
+    qt = z(E, K, N, dt=q8)
+    scale_t = z(E, (K + 127) // 128, abi.moe_fp8_scale_cols(N), dt=u8)
+    abi.moe_quant_weights_fp8(w, q, scale, qt, scale_t, stream=stream)
+    return q, scale, qt, scale_t
+
+
+def quantize_experts(w_gu, w_down, stream=None):
+    """The 8-bit weights that MoEBlock(fp8=True) takes as w_gu and w_down."""
+    return quantize_weights(w_gu, stream=stream), quantize_weights(w_down, stream=stream)
+
+
 class MoEBlock:
     def __init__(self, T: int, d: int, E: int, k: int, f: int, dtype=torch.bfloat16,
                  device="cuda", backward: bool = True, fuse_router_dx: bool = True,
                  lora_rank: int = 0, lora_scale: float = 1.0, gather: bool = False,
-                 store_x_perm: bool = True):
+                 store_x_perm: bool = True, router: Optional[ScoreRouter] = None,
+                 fp8: bool = False):
+        if fp8 and (backward or lora_rank or gather or dtype != torch.bfloat16):
+            raise ValueError("fp8 experts run forward only (backward=False), in bf16, without "
+                             "LoRA; their rows are gathered by themselves")
+        self.fp8, self.router = fp8, router
         if gather and (lora_rank or dtype != torch.bfloat16):
             raise ValueError("gather needs bf16 experts without LoRA")
         # beyond the gathered calls' limits the block runs on stored rows
@@ -62,7 +137,8 @@ class MoEBlock:
         if self.gather_fallback:
             gather = False
         self.gather = gather
-        self.store_x_perm = store_x_perm or not gather
+        fp8_gather = fp8 and gather_fits_fp8(T, d, k)
+        self.store_x_perm = not fp8_gather if fp8 else store_x_perm or not gather
         self.T, self.d, self.E, self.k, self.f = T, d, E, k, f
         self.fuse_router_dx = fuse_router_dx
         self.lora_rank, self.lora_scale = lora_rank, lora_scale
@@ -84,12 +160,21 @@ class MoEBlock:
         self.row_to_slot = z(R, dt=i32)
         self.x_perm = z(R, d) if self.store_x_perm else None
         self.w_perm = z(R, dt=f32)
-        self.gu = z(R, 2 * f)
-        self.h = z(R, f)
+        if fp8:
+            q8, u8 = torch.float8_e4m3fn, torch.uint8
+            rows = T if fp8_gather else R
+            self.x8 = z(rows, d, dt=q8)
+            self.x8_scale = z(rows, abi.moe_fp8_scale_cols(d), dt=u8)
+            self.gu = None
+            self.h = z(R, f, dt=q8)
+            self.h_scale = z(R, abi.moe_fp8_scale_cols(f), dt=u8)
+        else:
+            self.gu = z(R, 2 * f)
+            self.h = z(R, f)
         self.y_perm = z(R, d)
         self.y = z(T, d)
         ws_perm = abi.moe_permute_workspace_size(T, E, k)
-        ws_ffn = abi.moe_grouped_ffn_workspace_size(R, E, d, f, dc)
+        ws_ffn = 0 if fp8 else abi.moe_grouped_ffn_workspace_size(R, E, d, f, dc)
         ws_rtr = abi.moe_router_logits_bwd_workspace_size(T, d, E) if backward else 0
         ws_stat = max(abi.moe_expert_load_workspace_size(T, E, k),
                       abi.moe_aux_loss_workspace_size(T, E))
@@ -128,9 +213,12 @@ class MoEBlock:
     def forward(self, x, w_r, w_gu, w_down, bias=None, noise=None, stream=None, sel_bias=None,
                 lora=None):
         """bias is added to the logits (it moves selection and weights);
-        sel_bias only shifts the scores the top-k compares."""
+        sel_bias only shifts the scores the top-k compares.  With fp8, w_gu
+        and w_down are the pairs of quantize_experts()."""
         abi.moe_router_logits(x, w_r, bias, noise, self.logits, stream)
-        if sel_bias is None:
+        if self.router is not None:
+            self.router.forward(self.logits, sel_bias, self.k, self.topk_idx, self.topk_w, stream)
+        elif sel_bias is None:
             abi.moe_route(self.logits, self.k, self.topk_idx, self.topk_w, stream)
         else:
             abi.moe_route_biased(self.logits, sel_bias, self.k, self.topk_idx, self.topk_w, stream)
@@ -149,6 +237,14 @@ class MoEBlock:
     def experts_forward(self, w_gu, w_down, stream=None, lora=None, x=None):
         """lora: (a_gu, b_gu, a_dn, b_dn) device tensors when lora_rank is set;
         x: the token rows, read by the gathered GEMM."""
+        if self.fp8:
+            gathered = not self.store_x_perm
+            abi.moe_quant_rows_fp8(x if gathered else self.x_perm, self.x8, self.x8_scale, stream)
+            abi.moe_grouped_ffn_fwd_fp8(self.x8, self.x8_scale, self.offsets, *w_gu, *w_down,
+                                        self.w_perm, self.h, self.h_scale, self.y_perm,
+                                        row_to_slot=self.row_to_slot if gathered else None,
+                                        k=self.k, stream=stream)
+            return
         if self.gather:
             abi.moe_grouped_ffn_fwd_gather(x, self.row_to_slot, self.k, self.offsets, self.E,
                                            w_gu, w_down, self.w_perm, self.gu, self.h,
@@ -174,8 +270,12 @@ class MoEBlock:
         if not self.gather:
             abi.moe_combine_bwd(dy, self.slot_to_row, self.k, self.dy_perm, stream)
         self.experts_backward(w_gu, w_down, stream, lora, x=x, dy=dy)
-        abi.moe_route_bwd(self.topk_idx, self.topk_w, self.d_row_scale, self.slot_to_row,
-                          self.E, self.d_topk_w, self.d_logits, stream)
+        if self.router is not None:
+            self.router.backward(self.logits, self.topk_idx, self.topk_w, self.d_row_scale,
+                                 self.slot_to_row, self.d_topk_w, self.d_logits, stream)
+        else:
+            abi.moe_route_bwd(self.topk_idx, self.topk_w, self.d_row_scale, self.slot_to_row,
+                              self.E, self.d_topk_w, self.d_logits, stream)
         if aux_coeff != 0.0:
             n = self.T if n_valid is None else n_valid
             abi.moe_expert_load(self.topk_idx, n, self.E, self.load, self.ws, stream)
