@@ -6,7 +6,7 @@
 // 128 x 128 (weights); s is the smallest integer >= -127 that keeps the
 // block's largest finite magnitude within 448 * 2^s, so x * 2^-s is exact in
 // fp32 and the conversion is the one rounding.  The byte s + 127 is what
-// v_mfma_scale_f32_16x16x128_f8f6f4 takes as an operand: the scales of a
+// v_mfma_scale_f32_*_f8f6f4 takes as an operand: the scales of a
 // 128-wide K block enter the product inside the matrix instruction, and the
 // fp32 accumulator runs over all of K with no work between the blocks (an
 // arbitrary fp32 scale would need a multiply-add of every accumulator per
@@ -200,16 +200,19 @@ __global__ __launch_bounds__(256) void k_quant_weights(const T *__restrict__ w, 
 // over BP output columns (weight rows; in the gate/up product BP/2 gate rows
 // and the BP/2 up rows of the same features), q over BQ rows of one expert.
 // K runs in stages of 128 bytes, one scale block: both operands of a stage
-// go to LDS with direct loads of 16 bytes per lane, NS stages deep.
+// go to a ring in LDS with direct loads of 16 bytes per lane.
 //
 // LDS: operand row r of a stage is 8 chunks of 16 bytes, chunk c at place
 // c ^ ((r >> 1) & 7), so that the fragment reads (16 rows, one chunk each)
 // spread over the banks.
 //
-// MFMA 16x16x128: lane l holds 32 bytes of row l % 16 of each operand; which
-// of the 128 k they are does not matter as long as both operands agree and
-// share one scale per row: chunks g and g + 4 of the stage, g = l / 16.  The
-// result holds D[4 g + v][l % 16].
+// MFMA 16x16x128 (few rows): lane l holds 32 bytes of row l % 16 of each
+// operand; which of the 128 k they are does not matter as long as both
+// operands agree and share one scale per row: chunks g and g + 4 of the stage,
+// g = l / 16.  The result holds D[4 g + v][l % 16].
+// MFMA 32x32x64 (many rows): row l % 32, chunks g and g + 2 of the stage's
+// first 64 k and 4 + g, 6 + g of its last, g = l / 32; the result holds
+// D[8 (v / 4) + 4 g + v % 4][l % 32].
 struct Fp8Args {
   const uint8_t *a, *a_scale;     // rows [.., K], scales [.., scale_cols(K)]
   const int32_t *row_to_slot;     // gathered rows: row r is slot / k; or null
@@ -377,24 +380,103 @@ __device__ __forceinline__ i32x8_t frag(const LDS_AS char *lds, uint32_t at, uin
                  (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
 }
 
+// The same for the wide kernel's tiles of 256 x 256 and 8 waves, whose P rows
+// come as two halves (gate/up: gate and up rows) of two instructions per wave
+// each, and whose Q rows take four.
+template <bool GU>
+struct WideLoads {
+  static constexpr uint32_t HALF = 128 * 128, ROWS = 256 * 128;   // bytes of a P half, of the Q rows
+  static constexpr uint32_t STAGE = ROWS + 2 * HALF;              // Q rows, P half 0, P half 1
+  uint32_t voffP[2], voffQ[4];
+  uint32_t left[2];      // K minus the lane's chunk offset, by parity of the instruction
+  const uint8_t *pbase[2], *qbase;
+  uint32_t pbytes[2], qbytes;
+  uint32_t ldsP, ldsQ;   // the wave's places in the ring's first stage
+  int wave, lane;
+
+  __device__ __forceinline__ void init(const Fp8Args &g, int wave_, int lane_, const void *smem) {
+    wave = wave_;
+    lane = lane_;
+    ldsQ = lds_addr(smem) + (uint32_t)wave * 4096u;
+    ldsP = lds_addr(smem) + ROWS + (uint32_t)wave * 2048u;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) left[i] = (uint32_t)max(g.K - (int)chunk(i), 0);
+  }
+  // row (of the wave's) and byte of the chunk that a lane loads with instruction i
+  __device__ __forceinline__ int row(int i) const { return 8 * i + (lane >> 3); }
+  __device__ __forceinline__ uint32_t chunk(int i) const {
+    return (uint32_t)((lane & 7) ^ ((row(i) >> 1) & 7)) * 16u;
+  }
+  // src(r): the row of a (from qbase) that holds row r of the tile, or -1
+  template <typename Src>
+  __device__ __forceinline__ void tile(const Fp8Args &g, const Tile &t, Src src) {
+    const int K = g.K, p0 = t.pt * (GU ? 128 : 256);
+    const uint8_t *const first = g.b + ((GU ? 2 : 1) * (int64_t)g.N * t.e + p0) * K;
+    pbase[0] = first;
+    pbase[1] = first + (int64_t)(GU ? g.N : 128) * K;
+    pbytes[0] = (uint32_t)min(g.N - p0, 128) * (uint32_t)K;
+    pbytes[1] = GU ? pbytes[0] : (uint32_t)min(max(g.N - p0 - 128, 0), 128) * (uint32_t)K;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) voffP[i] = (uint32_t)(16 * wave + row(i)) * (uint32_t)K + chunk(i);
+    const bool gathered = g.row_to_slot != nullptr;
+    qbase = gathered ? g.a : g.a + ((int64_t)t.seg0 + t.q0) * K;
+    qbytes = gathered ? (uint32_t)(g.a_rows * K) : (uint32_t)t.qvalid * (uint32_t)K;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = src(32 * wave + row(i));
+      voffQ[i] = r >= 0 ? (uint32_t)r * (uint32_t)K + chunk(i) : kOOB;
+    }
+  }
+  // Instruction i of P half h / of the Q rows, of the stage at byte k0 of the
+  // rows, into the place of the ring at `buf`.
+  __device__ __forceinline__ void p(int h, int i, uint32_t k0, uint32_t buf) const {
+    dma16(make_rsrc(pbase[h] + k0, max(pbytes[h], k0) - k0),
+          ldsP + buf + (uint32_t)h * HALF + (uint32_t)i * 1024u, k0 < left[i] ? voffP[i] : kOOB);
+  }
+  __device__ __forceinline__ void q(int i, uint32_t k0, uint32_t buf) const {
+    dma16(make_rsrc(qbase + k0, max(qbytes, k0) - k0), ldsQ + buf + (uint32_t)i * 1024u,
+          k0 < left[i & 1] ? voffQ[i] : kOOB);
+  }
+  // Q rows and P half 0 (6 instructions), then P half 1 (2)
+  __device__ __forceinline__ void front(int i, uint32_t k0, uint32_t buf) const {
+    if (i < 4) q(i, k0, buf);
+    else p(0, i - 4, k0, buf);
+  }
+  __device__ __forceinline__ void issue(uint32_t k0, uint32_t buf) const {
+#pragma unroll
+    for (int i = 0; i < 6; ++i) front(i, k0, buf);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) p(1, i, k0, buf);
+  }
+};
+
 // Many rows: tiles of 256 x 256, 8 waves of 128 x 64 (4 x 2 fragments of
-// 32 x 32, MFMA 32x32x64: two steps per stage).  Persistent: one block of
-// threads per CU walks its tiles.
+// 32 x 32, MFMA 32x32x64).  Persistent: one block of threads per CU walks its
+// tiles.
 //
-// A wave's K steps are pipelined: while the MFMAs of a step run, the next
-// step's fragments come from LDS, the Q fragments into the other register
-// set, a P fragment into its own registers once its MFMAs are issued.  The
-// barrier that publishes a stage stands before the last step of the stage
-// before it, whose fragments are all in registers then, so that its place in
-// the ring takes the loads of the stage after the published one; they go out
-// between the MFMAs.  After a tile's last stage the next tile's first stage
-// and scales are loaded while the epilogue runs, which uses the ring's other
-// place.
+// A stage is worked on in two halves, its P rows 0 .. 127 and 128 .. 255 (gate
+// and up), each against all Q rows: 8 MFMAs of a wave.  While the MFMAs of a
+// half run, the next half's fragments come from LDS into the registers of
+// those that are done with (the Q fragments every other half).  A barrier
+// stands in the middle of each half: behind it the parts of the ring that the
+// half's own fragments came from are free, and the next half's have landed.
+// So a stage's Q rows and first P half are loaded three halves before they
+// are read, and its second P half too, with two stages in the ring: loads may
+// take one and a half stages.  After a tile's last stage the next tile's
+// first stage and scales are loaded while the epilogue runs, which uses the
+// ring's other place.
+//
+// 16384 rows x 32 experts, d = f = 2880: gate/up 545 GFLOP in 362 us, down 272
+// GFLOP in 198 us.  With the MFMAs taken out 251 us, with the loads taken out
+// 270 us (gate/up): neither alone bounds, and the clock falls under both.  One
+// barrier a stage, with loads one stage ahead, took 379 and 204 us; big and
+// small tiles dealt out separately, so that no CU gets one big tile more than
+// another, took longer (an expert's slab is then fetched twice).
 template <bool GU>
 __global__ __launch_bounds__(512, 2) void k_grouped_fp8_wide(Fp8Args g) {
-  constexpr int BP = 256, BQ = 256, WP = 2, NW = 8, NS = 2, FP = 4, FQ = 2;
-  using L = Loads<GU, BP, BQ, NW>;
-  __shared__ u32x4_t smem[NS * (L::TP + L::TQ)];
+  constexpr int BP = 256, BQ = 256, WP = 2, NW = 8, FP = 4, FQ = 2;
+  using L = WideLoads<GU>;
+  __shared__ u32x4_t smem[2 * L::STAGE / 16];
   __shared__ uint32_t s_qs[kScaleChunk / 4][BQ];   // scales of a chunk of K blocks, four to a dword
   __shared__ uint32_t s_ps[kScaleChunk / 4][4];
   __shared__ int s_slot[BQ];                        // gathered rows: the next tile's slots
@@ -454,7 +536,7 @@ __global__ __launch_bounds__(512, 2) void k_grouped_fp8_wide(Fp8Args g) {
 
   // ---- loads of a tile: its slots, its scales of a chunk of K blocks
   L ld;
-  ld.init(g, wave, lane, smem, 0);
+  ld.init(g, wave, lane, smem);
   auto load_slots = [&](const Tile &t) {
     if (wave < BQ / 64)
       dma4(make_rsrc(g.row_to_slot + t.seg0 + t.q0, (uint32_t)t.qvalid * 4u),
@@ -495,16 +577,15 @@ __global__ __launch_bounds__(512, 2) void k_grouped_fp8_wide(Fp8Args g) {
 
   // ---- fragments
   const int lr = lane & 31, lg = lane >> 5;
-  int prow[FP];   // first row in the tile; gate/up: fragments 0, 1 gate, 2, 3 up
+  int prow[FP];   // first row in the tile: fragments 0, 1 in half 0, fragments 2, 3 in half 1
 #pragma unroll
-  for (int i = 0; i < FP; ++i)
-    prow[i] = GU ? (i >> 1) * (BP / 2) + wp * 64 + 32 * (i & 1) : wp * 128 + 32 * i;
+  for (int i = 0; i < FP; ++i) prow[i] = (i >> 1) * 128 + wp * 64 + 32 * (i & 1);
   // Q fragment j: rows 32 wq + 128 j, so that a tile's last rows are spread
   // over the SIMDs
   const int qrow0 = wq * 32;
   const LDS_AS char *lds = (const LDS_AS char *)smem;
-  // lane's first chunk of step 0: row lr, chunk lg; step 1: chunk bit 2, the
-  // fragment's second chunk: bit 1
+  // lane's first chunk of the first 64 k: row lr, chunk lg; of the others:
+  // chunk bit 2; the fragment's second chunk: bit 1
   const uint32_t at0 = (uint32_t)lr * 128u + (uint32_t)((lg ^ ((lr >> 1) & 7)) * 16);
   Tile t = decode(id);
   if (gathered) load_slots(t);
@@ -538,11 +619,12 @@ __global__ __launch_bounds__(512, 2) void k_grouped_fp8_wide(Fp8Args g) {
     if (more && gathered) load_slots(tn);
     ld.issue(128, L::STAGE);
 
-    i32x8_t pf[FP], qf[2][FQ];
-    auto read_p = [&](int i, uint32_t at) { pf[i] = frag(lds + prow[i] * 128, at, 32u); };
-    auto read_q = [&](int set, uint32_t at) {
-#pragma unroll
-      for (int j = 0; j < FQ; ++j) qf[set][j] = frag(lds + L::TP * 16 + (qrow0 + 128 * j) * 128, at, 32u);
+    i32x8_t pf[2][2], qf[FQ][2];   // [row fragment][first or last 64 k]
+    auto read_p = [&](int h, int i, int s, uint32_t at) {
+      pf[i][s] = frag(lds + L::ROWS + prow[2 * h + i] * 128, at ^ (s ? 64u : 0u), 32u);
+    };
+    auto read_q = [&](int j, int s, uint32_t at) {
+      qf[j][s] = frag(lds + (qrow0 + 128 * j) * 128, at ^ (s ? 64u : 0u), 32u);
     };
     // scales: of the stage at hand in the lowest byte, of the next ones above it
     uint32_t sp[FP], sq[FQ], sp4[FP], sq4[FQ];
@@ -553,9 +635,13 @@ __global__ __launch_bounds__(512, 2) void k_grouped_fp8_wide(Fp8Args g) {
 #pragma unroll
       for (int j = 0; j < FQ; ++j) sq4[j] = s_qs[w][qrow0 + 128 * j + lr];
     };
-    read_q(0, at0);
 #pragma unroll
-    for (int i = 0; i < FP; ++i) read_p(i, at0);
+    for (int s = 0; s < 2; ++s) {
+#pragma unroll
+      for (int j = 0; j < FQ; ++j) read_q(j, s, at0);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) read_p(0, i, s, at0);
+    }
     scales(0);
 #pragma unroll
     for (int i = 0; i < FP; ++i) sp[i] = sp4[i];
@@ -565,46 +651,67 @@ __global__ __launch_bounds__(512, 2) void k_grouped_fp8_wide(Fp8Args g) {
     auto run = [&](auto nl) {
       constexpr int NL = decltype(nl)::value;
       uint32_t at = at0, k0 = 256;   // stage n's place; byte of stage n + 2
+      auto mfma = [&](int h, int i, int s) {
+#pragma unroll
+        for (int j = 0; j < NL; ++j)
+          acc[2 * h + i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+              pf[i][s], qf[j][s], acc[2 * h + i][j], 0, 0, 0, (int)sp[2 * h + i], 0, (int)sq[j]);
+      };
+      // What the next half reads has landed everywhere (8 younger loads are on
+      // their way), and what this half was read from is free.
+      auto publish = [&]() {
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+        wait_vm<8>();
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+      };
       for (int n = 0;;) {
         const int end = min(nk, (n / kScaleChunk + 1) * kScaleChunk);
         // (no branch in the body: the compiler would move MFMAs over it)
         for (; n < end; ++n) {
-          // step 0, and the reads of step 1's fragments
-          read_q(1, at ^ 64u);
-#pragma unroll
-          for (int i = 0; i < FP; ++i) {
-#pragma unroll
-            for (int j = 0; j < NL; ++j)
-              acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                  pf[i], qf[0][j], acc[i][j], 0, 0, 0, (int)sp[i], 0, (int)sq[j]);
-            __builtin_amdgcn_sched_barrier(0);
-            read_p(i, at ^ 64u);
-          }
-          // stage n + 1 has landed everywhere, and stage n is read (its last
-          // fragments are in registers): its place is free
-          asm volatile("" ::: "memory");
-          __builtin_amdgcn_sched_barrier(0);
-          wait_vm<0>();
-          __builtin_amdgcn_s_barrier();
-          asm volatile("" ::: "memory");
-          __builtin_amdgcn_sched_barrier(0);
-          // step 1, the reads of stage n + 1's step 0 and the loads of stage n + 2
           const uint32_t buf = n & 1 ? L::STAGE : 0u;
+          // half 0; half 1's P fragments follow; Q rows and P half 0 of stage n + 2
+          mfma(0, 0, 0);
+          mfma(0, 1, 0);
+          publish();
+          read_p(1, 0, 0, at);
+          read_p(1, 1, 0, at);
+          ld.front(0, k0, buf);
+          ld.front(1, k0, buf);
+          __builtin_amdgcn_sched_barrier(0);
+          mfma(0, 0, 1);
+          ld.front(2, k0, buf);
+          ld.front(3, k0, buf);
+          __builtin_amdgcn_sched_barrier(0);
+          read_p(1, 0, 1, at);
+          mfma(0, 1, 1);
+          ld.front(4, k0, buf);
+          ld.front(5, k0, buf);
+          __builtin_amdgcn_sched_barrier(0);
+          read_p(1, 1, 1, at);
+          // half 1; stage n + 1's half 0 and Q fragments follow; P half 1 of stage n + 2
           at ^= L::STAGE;
+          mfma(1, 0, 0);
+          mfma(1, 1, 0);
+          publish();
           scales(n + 1);
-          read_q(0, at);
-#pragma unroll
-          for (int i = 0; i < FP; ++i) {
-#pragma unroll
-            for (int j = 0; j < FQ; ++j) {
-              if (j < NL)
-                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                    pf[i], qf[1][j], acc[i][j], 0, 0, 0, (int)sp[i], 0, (int)sq[j]);
-              ld.one(2 * i + j, k0, buf);
-            }
-            __builtin_amdgcn_sched_barrier(0);
-            read_p(i, at);
-          }
+          read_q(0, 0, at);
+          read_q(1, 0, at);
+          read_p(0, 0, 0, at);
+          read_p(0, 1, 0, at);
+          ld.p(1, 0, k0, buf);
+          __builtin_amdgcn_sched_barrier(0);
+          mfma(1, 0, 1);
+          ld.p(1, 1, k0, buf);
+          __builtin_amdgcn_sched_barrier(0);
+          read_p(0, 0, 1, at);
+          mfma(1, 1, 1);
+          __builtin_amdgcn_sched_barrier(0);
+          read_p(0, 1, 1, at);
+          read_q(0, 1, at);
+          read_q(1, 1, at);
           k0 += 128;
           const bool fresh = ((n + 1) & 3) == 0;
 #pragma unroll
@@ -733,7 +840,7 @@ __global__ __launch_bounds__(512, 2) void k_grouped_fp8_wide(Fp8Args g) {
           const int row = rr + (ln >> 4), ch = ln & 15;
           const u32x4_t val =
               *reinterpret_cast<const LDS_AS u32x4_t *>(slot + row * 256 + (ch ^ (row & 15)) * 16);
-          const int qq = qrow0 + 128 * j + row, n = p0 + wp * 128 + 8 * ch;
+          const int qq = qrow0 + 128 * j + row, n = p0 + wp * 64 + (ch >> 3) * 128 + (ch & 7) * 8;
           if (qq < t.qvalid && n < N) *reinterpret_cast<u32x4_t *>(g.c + (r0 + qq) * N + n) = val;
         }
       }
@@ -949,8 +1056,8 @@ __global__ __launch_bounds__(512) void k_grouped_fp8_few(Fp8Args g) {
 
 // Rows per expert (on average, of those that can have rows) up to which the
 // few-rows kernel runs.  At d = f = 2880, 32 experts, gate/up + down: 105 + 58
-// us against the other's 128 + 82 at 8 rows, 111 + 65 against 133 + 85 at 32,
-// 154 + 91 against 145 + 93 at 64.
+// us against the other's 107 + 67 at 8 rows, 111 + 65 against 110 + 69 at 32,
+// 117 + 70 against 115 + 71 at 48, 134 + 80 against 117 + 72 at 56.
 constexpr int64_t kFewRows = 48;
 constexpr int kCUs = 256;   // persistent kernels: one block of threads per CU, a multiple of 8
 
