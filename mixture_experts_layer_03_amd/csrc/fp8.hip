@@ -282,6 +282,60 @@ struct Tile {
   int e, pt, q0, seg0, qvalid;
 };
 
+// Tiles are numbered expert, then output columns, then rows (fastest), BQ rows
+// each, and split into 8 contiguous chunks, one per XCD (blocks go round the
+// XCDs): the tiles in flight on an XCD share their weight slab in its L2.
+struct Tiles {
+  int off[kMaxExperts + 1];     // the experts' first rows, in [0, R]
+  int start[kMaxExperts + 1];   // the experts' first tiles
+  // by all threads of the block
+  template <int BQ>
+  __device__ __forceinline__ void init(const Fp8Args &g) {
+    const int lane = threadIdx.x & 63;
+    for (int i = threadIdx.x; i <= g.E; i += blockDim.x)
+      off[i] = (int)min(max((int64_t)g.offsets[i], (int64_t)0), g.slots);
+    __syncthreads();
+    if (threadIdx.x < 64) {
+      int base = 0;
+      for (int e0 = 0; e0 < g.E; e0 += 64) {
+        const int e = e0 + lane;
+        int n = e < g.E ? (max(off[e + 1] - off[e], 0) + BQ - 1) / BQ * g.PT : 0;
+#pragma unroll
+        for (int m = 1; m < 64; m <<= 1) {
+          const int o = __shfl_up(n, m, 64);
+          if (lane >= m) n += o;
+        }
+        if (e < g.E) start[e + 1] = base + n;
+        base += __builtin_amdgcn_readlane(n, 63);
+      }
+      if (lane == 0) start[0] = 0;
+    }
+    __syncthreads();
+  }
+  __device__ __forceinline__ int total(const Fp8Args &g) const {
+    return __builtin_amdgcn_readfirstlane(start[g.E]);
+  }
+  template <int BQ>
+  __device__ __forceinline__ Tile decode(const Fp8Args &g, int at) const {
+    const int lane = threadIdx.x & 63;
+    for (int e0 = 0;; e0 += 64) {
+      const uint64_t hit = __ballot(e0 + lane < g.E && start[min(e0 + lane, g.E - 1) + 1] > at);
+      if (hit) {
+        Tile t;
+        t.e = __builtin_amdgcn_readfirstlane(e0 + __ffsll((unsigned long long)hit) - 1);
+        t.seg0 = __builtin_amdgcn_readfirstlane(off[t.e]);
+        const int rows = __builtin_amdgcn_readfirstlane(off[t.e + 1]) - t.seg0;
+        const int qt = (rows + BQ - 1) / BQ;
+        const int in = at - __builtin_amdgcn_readfirstlane(start[t.e]);
+        t.pt = in / qt;
+        t.q0 = (in % qt) * BQ;
+        t.qvalid = min(rows - t.q0, BQ);
+        return t;
+      }
+    }
+  }
+};
+
 // The direct loads of a tile's K stages.  Instruction i of a wave covers 8
 // rows x 128 bytes; a lane's byte offset is fixed for the tile and the
 // resource's base moves with the stage.  Chunks past K read nothing, and so
@@ -481,7 +535,7 @@ __global__ __launch_bounds__(512, 2) void k_grouped_fp8_wide(Fp8Args g) {
   __shared__ uint32_t s_ps[kScaleChunk / 4][4];
   __shared__ int s_slot[BQ];                        // gathered rows: the next tile's slots
   __shared__ float s_amax[GU ? WP : 1][GU ? BQ : 1];
-  __shared__ int s_off[kMaxExperts + 1], s_ts[kMaxExperts + 1];
+  __shared__ Tiles tiles;
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -489,50 +543,12 @@ __global__ __launch_bounds__(512, 2) void k_grouped_fp8_wide(Fp8Args g) {
   const int N = g.N, nk = scale_blocks(g.K), cols = scale_cols(g.K);
   const bool gathered = g.row_to_slot != nullptr;
 
-  // ---- tiles.  Numbered expert, then output columns, then rows (fastest),
-  // split into 8 contiguous chunks, one per XCD (blocks go round the XCDs):
-  // the tiles in flight on an XCD share their weight slab in its L2.
-  for (int i = tid; i <= g.E; i += NW * 64)
-    s_off[i] = (int)min(max((int64_t)g.offsets[i], (int64_t)0), g.slots);
-  __syncthreads();
-  if (wave == 0) {
-    int base = 0;
-    for (int e0 = 0; e0 < g.E; e0 += 64) {
-      const int e = e0 + lane;
-      int n = e < g.E ? (max(s_off[e + 1] - s_off[e], 0) + BQ - 1) / BQ * g.PT : 0;
-#pragma unroll
-      for (int m = 1; m < 64; m <<= 1) {
-        const int o = __shfl_up(n, m, 64);
-        if (lane >= m) n += o;
-      }
-      if (e < g.E) s_ts[e + 1] = base + n;
-      base += __builtin_amdgcn_readlane(n, 63);
-    }
-    if (lane == 0) s_ts[0] = 0;
-  }
-  __syncthreads();
-  const int total = __builtin_amdgcn_readfirstlane(s_ts[g.E]);
+  tiles.template init<BQ>(g);
+  const int total = tiles.total(g);
   const int per = (int)(gridDim.x >> 3), chunk = (total + 7) >> 3;
   const int cend = min(total, ((int)(blockIdx.x & 7) + 1) * chunk);
   int id = (int)(blockIdx.x & 7) * chunk + (int)(blockIdx.x >> 3);
   if (id >= cend) return;
-  auto decode = [&](int at) -> Tile {
-    for (int e0 = 0;; e0 += 64) {
-      const uint64_t hit = __ballot(e0 + lane < g.E && s_ts[min(e0 + lane, g.E - 1) + 1] > at);
-      if (hit) {
-        Tile t;
-        t.e = __builtin_amdgcn_readfirstlane(e0 + __ffsll((unsigned long long)hit) - 1);
-        t.seg0 = __builtin_amdgcn_readfirstlane(s_off[t.e]);
-        const int rows = __builtin_amdgcn_readfirstlane(s_off[t.e + 1]) - t.seg0;
-        const int qt = (rows + BQ - 1) / BQ;
-        const int in = at - __builtin_amdgcn_readfirstlane(s_ts[t.e]);
-        t.pt = in / qt;
-        t.q0 = (in % qt) * BQ;
-        t.qvalid = min(rows - t.q0, BQ);
-        return t;
-      }
-    }
-  };
 
   // ---- loads of a tile: its slots, its scales of a chunk of K blocks
   L ld;
@@ -587,7 +603,7 @@ __global__ __launch_bounds__(512, 2) void k_grouped_fp8_wide(Fp8Args g) {
   // lane's first chunk of the first 64 k: row lr, chunk lg; of the others:
   // chunk bit 2; the fragment's second chunk: bit 1
   const uint32_t at0 = (uint32_t)lr * 128u + (uint32_t)((lg ^ ((lr >> 1) & 7)) * 16);
-  Tile t = decode(id);
+  Tile t = tiles.template decode<BQ>(g, id);
   if (gathered) load_slots(t);
   wait_vm<0>();
   __syncthreads();
@@ -599,7 +615,7 @@ __global__ __launch_bounds__(512, 2) void k_grouped_fp8_wide(Fp8Args g) {
     const int next = id + per;
     const bool more = next < cend;
     Tile tn = t;
-    if (more) tn = decode(next);
+    if (more) tn = tiles.template decode<BQ>(g, next);
     f32x16_t acc[FP][FQ];
 #pragma unroll
     for (int i = 0; i < FP; ++i)
@@ -852,56 +868,42 @@ __global__ __launch_bounds__(512, 2) void k_grouped_fp8_wide(Fp8Args g) {
   }
 }
 
-// Few rows per expert: the weights' way from memory bounds.  A block of
-// threads takes 256 weight rows (gate/up: 128 gate and 128 up, one block of
-// h; else BP) against up to BQ rows of an expert at a time, over all of K,
-// with NS - 1 stages on their way, and walks on by BQ rows if the expert has
-// more.  8 waves side by side along the weight rows, 16 x 16 fragments (MFMA
-// 16x16x128, one per stage and fragment pair).
-template <bool GU, int BP, int BQ, int NS>
-__global__ __launch_bounds__(512) void k_grouped_fp8_few(Fp8Args g) {
-  constexpr int NW = 8, FP = BP / NW / 16, FQ = BQ / 16;
+// Few rows per expert, where the weights' way from memory bounds, and few
+// tiles, where one tile's latency does: tiles of BP weight rows (gate/up: 128
+// gate and 128 up, one block of h) and 64 rows, a block of threads each, over
+// all of K with NS - 1 stages on their way.  NW waves side by side along the
+// weight rows, 16 x 16 fragments (MFMA 16x16x128, one per stage and fragment
+// pair; fragments past the expert's last row are left out).
+//
+// One CU draws about 50 GB/s from memory however much it has on its way, so
+// few rows want many tiles: d = f = 2880, 32 experts, BP = 64 against 128, down
+// product: 28 against 30 us at 4 tokens, 49 against 53 at 16, 57 against 58 at
+// 64 (265 MB: 4.7 TB/s).  More rows want more work per byte loaded: 1024 rows,
+// 8 experts, 608 x 608: 9.1 and 9.4 us; 4096 rows: 15.7 and 11.8 us.
+template <bool GU, int BP, int NS, int NW>
+__global__ __launch_bounds__(NW * 64) void k_grouped_fp8_small(Fp8Args g) {
+  constexpr int BQ = 64, FP = BP / NW / 16, FQ = BQ / 16;
   using L = Loads<GU, BP, BQ, NW>;
   static_assert(!GU || BP == 256, "a gate/up tile holds one block of 128 h");
   static_assert((NS - 2) * L::LOADS < 64, "vmcnt range");
   __shared__ u32x4_t smem[NS * (L::TP + L::TQ) + 64];
-  __shared__ uint32_t s_qs[kScaleChunk / 4][64];
+  __shared__ uint32_t s_qs[kScaleChunk / 4][BQ];
   __shared__ uint32_t s_ps[kScaleChunk / 4][4];
   __shared__ float s_amax[GU ? NW : 1][GU ? BQ : 1];
+  static_assert(sizeof(Tiles) <= sizeof(smem), "the tables share the ring");
+  Tiles &tiles = *reinterpret_cast<Tiles *>(smem);
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int N = g.N, nk = scale_blocks(g.K), cols = scale_cols(g.K);
   const bool gathered = g.row_to_slot != nullptr;
 
-  // the (blockIdx.y)-th expert that has rows
-  Tile t;
-  int rows = 0;
-  {
-    int want = (int)blockIdx.y;
-    t.e = -1;
-    for (int e0 = 0; e0 < g.E && t.e < 0; e0 += 64) {
-      int a = 0, n = 0;
-      if (e0 + lane < g.E) {
-        a = (int)min(max((int64_t)g.offsets[e0 + lane], (int64_t)0), g.slots);
-        n = (int)min(max((int64_t)g.offsets[e0 + lane + 1], (int64_t)0), g.slots) - a;
-      }
-      uint64_t full = __ballot(n > 0);
-      const int here = __popcll(full);
-      if (want >= here) {
-        want -= here;
-        continue;
-      }
-      for (; want > 0; --want) full &= full - 1;
-      const int l = __ffsll((unsigned long long)full) - 1;
-      t.e = e0 + l;
-      t.seg0 = __builtin_amdgcn_readlane(a, l);
-      rows = __builtin_amdgcn_readlane(n, l);
-    }
-    if (t.e < 0) return;
-    t.e = __builtin_amdgcn_readfirstlane(t.e);
-  }
-  t.pt = (int)blockIdx.x;
+  tiles.template init<BQ>(g);
+  const int total = tiles.total(g), chunk = (total + 7) >> 3;
+  const int id = (int)(blockIdx.x & 7) * chunk + (int)(blockIdx.x >> 3);
+  if ((int)(blockIdx.x >> 3) >= chunk || id >= total) return;
+  const Tile t = tiles.template decode<BQ>(g, id);
+  __syncthreads();   // the tables give way to the ring
   const int p0 = t.pt * (GU ? BP / 2 : BP);
   const int lr = lane & 15, lg = lane >> 4;
   int prow[FP], pblk[FP];
@@ -915,167 +917,172 @@ __global__ __launch_bounds__(512) void k_grouped_fp8_few(Fp8Args g) {
   L ld;
   ld.init(g, wave, lane, smem, NS * L::STAGE);
 
-  for (t.q0 = 0; t.q0 < rows; t.q0 += BQ) {
-    t.qvalid = min(rows - t.q0, BQ);
-    auto src = [&](int r) -> int {   // row of a, -1 past the segment or for no token
-      if (r >= t.qvalid) return -1;
-      if (!gathered) return r;
-      const uint32_t slot = (uint32_t)g.row_to_slot[(int64_t)t.seg0 + t.q0 + r];
-      return slot < (uint64_t)g.slots ? (int)(((uint64_t)slot * g.kmagic) >> 32) : -1;
-    };
-    const int srow = src(lane);
-    ld.tile(g, t, src);
-#pragma unroll
-    for (int n = 0; n < NS - 1; ++n) ld.issue(128u * n, n * L::STAGE);
-    auto load_scales = [&](int kc) {   // as in the wide kernel; one row per lane
-      const int nd = min(kScaleChunk, cols - kc) >> 2;
-      const u32x4_t rs =
-          gathered ? make_rsrc(g.a_scale, (uint32_t)(g.a_rows * cols))
-                   : make_rsrc(g.a_scale + ((int64_t)t.seg0 + t.q0) * cols, (uint32_t)(t.qvalid * cols));
-      for (int w = wave; w < nd; w += NW)
-        dma4(rs, lds_addr(&s_qs[w][0]), srow >= 0 ? (uint32_t)srow * (uint32_t)cols + (uint32_t)(kc + 4 * w) : kOOB);
-      if (wave == 0) {
-        const int mbs = scale_blocks((GU ? 2 : 1) * N);
-        const int b = lane & 3, w = lane >> 2;
-        const int first = GU && b > 0 ? (N + p0) / kBlk + b - 1 : p0 / kBlk + b;
-        dma4(make_rsrc(g.b_scale + (int64_t)t.e * mbs * cols, (uint32_t)(mbs * cols)), lds_addr(s_ps),
-             first < mbs && w < nd ? (uint32_t)(first * cols + kc + 4 * w) : kOOB);
-      }
-    };
-    load_scales(0);
-    f32x4_t acc[FP][FQ];
-#pragma unroll
-    for (int i = 0; i < FP; ++i)
-#pragma unroll
-      for (int j = 0; j < FQ; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    wait_vm<0>();   // the scales, and with them the first stages
-    __builtin_amdgcn_s_barrier();
-    uint32_t buf = 0, last = (NS - 1) * L::STAGE;   // places of stage n and of stage n + NS - 1
-    const int nlive = (t.qvalid + 15) >> 4;
-    for (int n = 0; n < nk; ++n) {
-      if (n > 0 && n % kScaleChunk == 0) {
-        wait_lgkm();
-        __builtin_amdgcn_s_barrier();
-        load_scales(n);
-        wait_vm<0>();
-      }
-      // stage n has landed everywhere and stage n - 1 is read
-      asm volatile("" ::: "memory");
-      wait_vm<(NS - 2) * L::LOADS>();
-      __builtin_amdgcn_s_barrier();
-      asm volatile("" ::: "memory");
-      ld.issue(128u * (n + NS - 1), last);
-      const int w = (n % kScaleChunk) >> 2, sh = (n & 3) * 8;
-      i32x8_t pf[FP];
-      uint32_t sp[FP];
-#pragma unroll
-      for (int i = 0; i < FP; ++i) {
-        pf[i] = frag(lds + prow[i] * 128, buf + at0, 64u);
-        sp[i] = s_ps[w][pblk[i]] >> sh;
-      }
-#pragma unroll
-      for (int j = 0; j < FQ; ++j) {
-        if (j < nlive) {
-          const i32x8_t qf = frag(lds + L::TP * 16 + 16 * j * 128, buf + at0, 64u);
-          const uint32_t sq = s_qs[w][16 * j + lr] >> sh;
-#pragma unroll
-          for (int i = 0; i < FP; ++i)
-            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                pf[i], qf, acc[i][j], 0, 0, 0, (int)sp[i], 0, (int)sq);
-        }
-      }
-      buf = buf == (NS - 1) * L::STAGE ? 0u : buf + L::STAGE;
-      last = last == (NS - 1) * L::STAGE ? 0u : last + L::STAGE;
+  auto src = [&](int r) -> int {   // row of a, -1 past the segment or for no token
+    if (r >= t.qvalid) return -1;
+    if (!gathered) return r;
+    const uint32_t slot = (uint32_t)g.row_to_slot[(int64_t)t.seg0 + t.q0 + r];
+    return slot < (uint64_t)g.slots ? (int)(((uint64_t)slot * g.kmagic) >> 32) : -1;
+  };
+  const int srow = src(lane);
+  ld.tile(g, t, src);
+  auto load_scales = [&](int kc) {   // as in the wide kernel
+    const int nd = min(kScaleChunk, cols - kc) >> 2;
+    const u32x4_t rs =
+        gathered ? make_rsrc(g.a_scale, (uint32_t)(g.a_rows * cols))
+                 : make_rsrc(g.a_scale + ((int64_t)t.seg0 + t.q0) * cols, (uint32_t)(t.qvalid * cols));
+    for (int w = wave; w < nd; w += NW)
+      dma4(rs, lds_addr(&s_qs[w][0]), srow >= 0 ? (uint32_t)srow * (uint32_t)cols + (uint32_t)(kc + 4 * w) : kOOB);
+    if (wave == 0) {
+      const int mbs = scale_blocks((GU ? 2 : 1) * N);
+      const int b = lane & 3, w = lane >> 2;
+      const int first = GU && b > 0 ? (N + p0) / kBlk + b - 1 : p0 / kBlk + b;
+      dma4(make_rsrc(g.b_scale + (int64_t)t.e * mbs * cols, (uint32_t)(mbs * cols)), lds_addr(s_ps),
+           first < mbs && w < nd ? (uint32_t)(first * cols + kc + 4 * w) : kOOB);
     }
-    asm volatile("" ::: "memory");
-    wait_vm<0>();
-    __builtin_amdgcn_s_barrier();   // every wave is done with the ring and the scales
-    asm volatile("" ::: "memory");
-
-    // Epilogue.  Lane holds D[4 lg + v][lr] of each fragment.
-    const int64_t r0 = (int64_t)t.seg0 + t.q0;
-    if constexpr (GU) {
+  };
+  load_scales(0);
 #pragma unroll
-      for (int j = 0; j < FQ; ++j) {
-        float m = 0.0f;
+  for (int n = 0; n < NS - 1; ++n) ld.issue(128u * n, n * L::STAGE);
+  f32x4_t acc[FP][FQ];
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          acc[0][j][v] = swiglu(acc[0][j][v], acc[1][j][v]);
-          m = fmaxf(m, finite_abs(acc[0][j][v]));
-        }
-        m = fmaxf(m, __shfl_xor(m, 16, 64));
-        m = fmaxf(m, __shfl_xor(m, 32, 64));
-        if (lane < 16) s_amax[wave][16 * j + lane] = m;
-      }
+  for (int i = 0; i < FP; ++i)
+#pragma unroll
+    for (int j = 0; j < FQ; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  uint32_t buf = 0, last = (NS - 1) * L::STAGE;   // places of stage n and of stage n + NS - 1
+  const int nlive = (t.qvalid + 15) >> 4;
+  for (int n = 0; n < nk; ++n) {
+    if (n > 0 && n % kScaleChunk == 0) {
       wait_lgkm();
       __builtin_amdgcn_s_barrier();
-      asm volatile("" ::: "memory");
-      const int hcols = scale_cols(N);
+      load_scales(n);
+      wait_vm<0>();
+    }
+    // stage n (and the scales, before it) has landed everywhere and stage n - 1 is read
+    asm volatile("" ::: "memory");
+    wait_vm<(NS - 2) * L::LOADS>();
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    ld.issue(128u * (n + NS - 1), last);
+    const int w = (n % kScaleChunk) >> 2, sh = (n & 3) * 8;
+    i32x8_t pf[FP];
+    uint32_t sp[FP];
 #pragma unroll
-      for (int j = 0; j < FQ; ++j) {
-        const int q = 16 * j + lr;
-        float m = 0.0f;
+    for (int i = 0; i < FP; ++i) {
+      pf[i] = frag(lds + prow[i] * 128, buf + at0, 64u);
+      sp[i] = s_ps[w][pblk[i]] >> sh;
+    }
 #pragma unroll
-        for (int i = 0; i < NW; ++i) m = fmaxf(m, s_amax[i][q]);
-        const uint32_t byte = scale_byte(m);
-        const float inv = inv_scale(byte);
-        if (q < t.qvalid) {
-          const int n = p0 + prow[0] + 4 * lg;
-          if (n < N)
-            *reinterpret_cast<uint32_t *>(g.h + (r0 + q) * N + n) =
-                pack_e4m3x4(scaled(acc[0][j][0], inv), scaled(acc[0][j][1], inv),
-                            scaled(acc[0][j][2], inv), scaled(acc[0][j][3], inv));
-          if (wave == 0 && lg == 0) {
-            g.h_scale[(r0 + q) * hcols + t.pt] = (uint8_t)byte;
-            if (t.pt == g.PT - 1)
-              for (int b = t.pt + 1; b < hcols; ++b) g.h_scale[(r0 + q) * hcols + b] = 127;
-          }
-        }
+    for (int j = 0; j < FQ; ++j) {
+      if (j < nlive) {
+        const i32x8_t qf = frag(lds + L::TP * 16 + 16 * j * 128, buf + at0, 64u);
+        const uint32_t sq = s_qs[w][16 * j + lr] >> sh;
+#pragma unroll
+        for (int i = 0; i < FP; ++i)
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+              pf[i], qf, acc[i][j], 0, 0, 0, (int)sp[i], 0, (int)sq);
       }
-    } else {
+    }
+    buf = buf == (NS - 1) * L::STAGE ? 0u : buf + L::STAGE;
+    last = last == (NS - 1) * L::STAGE ? 0u : last + L::STAGE;
+  }
+  asm volatile("" ::: "memory");
+  wait_vm<0>();
+  __builtin_amdgcn_s_barrier();   // every wave is done with the ring and the scales
+  asm volatile("" ::: "memory");
+
+  // Epilogue.  Lane holds D[4 lg + v][lr] of each fragment.
+  const int64_t r0 = (int64_t)t.seg0 + t.q0;
+  if constexpr (GU) {
 #pragma unroll
-      for (int j = 0; j < FQ; ++j) {
-        const int q = 16 * j + lr;
-        if (q >= t.qvalid) continue;
-        const float w = g.row_scale ? g.row_scale[r0 + q] : 1.0f;
+    for (int j = 0; j < FQ; ++j) {
+      float m = 0.0f;
 #pragma unroll
-        for (int i = 0; i < FP; ++i) {
-          const int n = p0 + prow[i] + 4 * lg;
-          if (n < N)
-            *reinterpret_cast<u32x2_t *>(g.c + (r0 + q) * N + n) =
-                u32x2_t{pack_bf16x2(w * acc[i][j][0], w * acc[i][j][1]),
-                        pack_bf16x2(w * acc[i][j][2], w * acc[i][j][3])};
+      for (int v = 0; v < 4; ++v) {
+        acc[0][j][v] = swiglu(acc[0][j][v], acc[1][j][v]);
+        m = fmaxf(m, finite_abs(acc[0][j][v]));
+      }
+      m = fmaxf(m, __shfl_xor(m, 16, 64));
+      m = fmaxf(m, __shfl_xor(m, 32, 64));
+      if (lane < 16) s_amax[wave][16 * j + lane] = m;
+    }
+    wait_lgkm();
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    const int hcols = scale_cols(N);
+#pragma unroll
+    for (int j = 0; j < FQ; ++j) {
+      const int q = 16 * j + lr;
+      float m = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NW; ++i) m = fmaxf(m, s_amax[i][q]);
+      const uint32_t byte = scale_byte(m);
+      const float inv = inv_scale(byte);
+      if (q < t.qvalid) {
+        const int n = p0 + prow[0] + 4 * lg;
+        if (n < N)
+          *reinterpret_cast<uint32_t *>(g.h + (r0 + q) * N + n) =
+              pack_e4m3x4(scaled(acc[0][j][0], inv), scaled(acc[0][j][1], inv),
+                          scaled(acc[0][j][2], inv), scaled(acc[0][j][3], inv));
+        if (wave == 0 && lg == 0) {
+          g.h_scale[(r0 + q) * hcols + t.pt] = (uint8_t)byte;
+          if (t.pt == g.PT - 1)
+            for (int b = t.pt + 1; b < hcols; ++b) g.h_scale[(r0 + q) * hcols + b] = 127;
         }
       }
     }
-    // the next rows' loads and scales must not pass this block's reads of s_amax
-    wait_lgkm();
-    __builtin_amdgcn_s_barrier();
+  } else {
+#pragma unroll
+    for (int j = 0; j < FQ; ++j) {
+      const int q = 16 * j + lr;
+      if (q >= t.qvalid) continue;
+      const float w = g.row_scale ? g.row_scale[r0 + q] : 1.0f;
+#pragma unroll
+      for (int i = 0; i < FP; ++i) {
+        const int n = p0 + prow[i] + 4 * lg;
+        if (n < N)
+          *reinterpret_cast<u32x2_t *>(g.c + (r0 + q) * N + n) =
+              u32x2_t{pack_bf16x2(w * acc[i][j][0], w * acc[i][j][1]),
+                      pack_bf16x2(w * acc[i][j][2], w * acc[i][j][3])};
+      }
+    }
   }
 }
 
 // Rows per expert (on average, of those that can have rows) up to which the
-// few-rows kernel runs.  At d = f = 2880, 32 experts, gate/up + down: 105 + 58
-// us against the other's 107 + 67 at 8 rows, 111 + 65 against 110 + 69 at 32,
-// 117 + 70 against 115 + 71 at 48, 134 + 80 against 117 + 72 at 56.
-constexpr int64_t kFewRows = 48;
+// weights bound.  d = f = 2880, 32 experts, gate/up + down, small tiles (BP =
+// 64) against the wide kernel: 104 + 57 us against 107 + 67 at 8 rows, 110 + 67
+// against 111 + 69 at 32, 116 + 74 against 115 + 71 at 48.
+constexpr int64_t kFewRows = 32;
 constexpr int kCUs = 256;   // persistent kernels: one block of threads per CU, a multiple of 8
+
+template <bool GU, int BP, int NS, int NW>
+int launch_small(Fp8Args g, int64_t active, const char *name, const char *fn, hipStream_t s) {
+  constexpr int per = GU ? BP / 2 : BP;
+  g.PT = (g.N + per - 1) / per;
+  // an expert ends with a partial tile at most
+  const int64_t tiles = (g.slots / 64 + active) * g.PT;
+  MOE_REQUIRE(tiles < ((int64_t)1 << 30), MOE_ERR_UNSUPPORTED, "%s: too many tiles", fn);
+  const unsigned blocks = (unsigned)((tiles + 7) / 8 * 8);
+  MOE_LAUNCH(name, s, (k_grouped_fp8_small<GU, BP, NS, NW><<<blocks, NW * 64, 0, s>>>(g)));
+  return check_launch(fn);
+}
 
 template <bool GU>
 int product(const Fp8Args &args, const char *name, const char *fn, hipStream_t s) {
   Fp8Args g = args;
   const int64_t active = g.E < g.slots ? (int64_t)g.E : g.slots;   // experts with rows, at most
-  if (g.slots <= kFewRows * active) {
-    constexpr int BP = GU ? 256 : 128;
-    const int per = 128;
-    g.PT = (g.N + per - 1) / per;
-    const dim3 grid((unsigned)g.PT, (unsigned)active);
-    MOE_LAUNCH(name, s, (k_grouped_fp8_few<GU, BP, 64, GU ? 3 : 5><<<grid, 512, 0, s>>>(g)));
-    return check_launch(fn);
-  }
+  if (g.slots <= kFewRows * active) return launch_small<GU, GU ? 256 : 64, GU ? 3 : 4, GU ? 8 : 4>(g, active, name, fn, s);
+  // Many rows, but so few small tiles (counting half a tile of 64 rows lost per
+  // expert) that all run at once: gate/up one, else two blocks of threads to a
+  // CU.  Event times against the wide kernel's: 608 x 608, 8 experts, 2048 rows
+  // (180 tiles) 12.8 against 17.7 us gate/up, (180) 9.5 against 15.8; 4096 rows
+  // (340) 21.5 against 18.8 and (340) 11.8 against 16.4; 8192 rows (660) 18.4
+  // against 17.9; 1024 rows, 4 experts, 2880 x 2880 (414) 51 against 42 and 27
+  // against 37; 2048 rows (782) 44 against 39.
+  const int64_t small = (g.slots / 64 + active / 2) * ((g.N + 127) / 128);
+  if (small <= (GU ? kCUs : 2 * kCUs)) return launch_small<GU, GU ? 256 : 128, 3, 8>(g, active, name, fn, s);
   const int per = GU ? 128 : 256;
   g.PT = (g.N + per - 1) / per;
-  // tile numbers are 32-bit; an expert ends with a partial tile at most
   const int64_t tiles = (g.slots / 256 + active) * g.PT;
   MOE_REQUIRE(tiles < ((int64_t)1 << 30), MOE_ERR_UNSUPPORTED, "%s: too many tiles", fn);
   const unsigned blocks = (unsigned)min((tiles + 7) / 8 * 8, (int64_t)kCUs);
