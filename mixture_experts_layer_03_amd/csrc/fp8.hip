@@ -344,7 +344,18 @@ struct Tiles {
 // rows x 128 bytes; a lane's byte offset is fixed for the tile and the
 // resource's base moves with the stage.  Chunks past K read nothing, and so
 // does every chunk of a stage past the last one: such a stage leaves zeros.
-template <bool GU, int BP, int BQ, int NW>
+//
+// LATE, for K = 64 mod 128, where every second row begins in the middle of a
+// 128-byte line: such a weight row is `late`.  Its stage n is bytes 128 n + 64
+// .., a whole line, its first 64 bytes come as the second half of a stage -1
+// (pre), and fragments are put together from the last stage's second half and
+// this stage's first.  Stages that straddle lines ask for every such line
+// twice: 92 blocks of threads reading 256 rows of 2880 bytes take 19.5 us, of
+// 2944 bytes 14.8.  The gate/up product of few rows has it (d = f = 2880, 32
+// experts: 28.9 -> 25.1 us at one token, 108 -> 104 at 64, 115 -> 109 at 256);
+// in the product into d its start costs as much as it saves (13.8 -> 15.4,
+// 59.5 -> 59.0).
+template <bool GU, int BP, int BQ, int NW, bool LATE>
 struct Loads {
   static constexpr int TP = BP * 8, TQ = BQ * 8;               // 16-byte chunks of a stage
   static constexpr int NIP = TP / 64 / NW;                     // instructions per wave and stage
@@ -357,7 +368,7 @@ struct Loads {
   static_assert(NIP * 64 * NW == TP && (NIQ == 1 || NIQ % 2 == 0), "loads per wave");
   static_assert(NIP % 2 == 0, "the chunk a lane loads depends on its place's parity alone");
   uint32_t voffP[NIP], voffQ[NIQ];
-  uint32_t leftP[2], leftQ[NIQ == 1 ? 1 : 2];   // K minus the lane's chunk offset, by parity of i
+  uint32_t leftP[2], leftQ[NIQ == 1 ? 1 : 2];   // K minus the lane's first byte, by parity of i
   uint32_t spare;        // byte behind the ring
   const uint8_t *pbase, *qbase;
   uint32_t pbytes, qbytes;
@@ -371,15 +382,15 @@ struct Loads {
     ldsP = lds_addr(smem) + (uint32_t)wave * (NIP * 1024u);
     ldsQ = lds_addr(smem) + TP * 16u + (uint32_t)wave * (NIQ * 1024u);
     spare = lds_addr(smem) + ring;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) leftP[i] = (uint32_t)max(g.K - (int)chunk(NIP * wave + i), 0);
-#pragma unroll
-    for (int i = 0; i < (NIQ == 1 ? 1 : 2); ++i) leftQ[i] = (uint32_t)max(g.K - (int)chunk(NIQ * wave + i), 0);
   }
   // row and byte of the chunk that a lane loads with instruction q of an operand
   __device__ __forceinline__ int row(int q) const { return 8 * q + (lane >> 3); }
   __device__ __forceinline__ uint32_t chunk(int q) const {
     return (uint32_t)((lane & 7) ^ ((row(q) >> 1) & 7)) * 16u;
+  }
+  // whether a row that begins at p is late
+  static __device__ __forceinline__ bool late(const Fp8Args &g, const uint8_t *p) {
+    return LATE && g.K % 64 == 0 && ((uintptr_t)p & 64);
   }
   // src(r): the row of a (from qbase) that holds row r of the tile, or -1
   template <typename Src>
@@ -392,9 +403,12 @@ struct Loads {
     const int64_t nmat = GU ? 2 * (int64_t)g.N : g.N;
     pbase = g.b + (t.e * nmat + p0 + (second ? g.N : 0)) * K;
     pbytes = (uint32_t)min(g.N - p0, GU ? BP / 2 : BP) * (uint32_t)K;
+    const uint32_t ahead = late(g, pbase + (lane >> 3) * K) ? 64u : 0u;   // rows 8 apart are alike
 #pragma unroll
     for (int i = 0; i < NIP; ++i)
-      voffP[i] = (uint32_t)(row(NIP * wave + i) - shift) * (uint32_t)K + chunk(NIP * wave + i);
+      voffP[i] = (uint32_t)(row(NIP * wave + i) - shift) * (uint32_t)K + chunk(NIP * wave + i) + ahead;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) leftP[i] = (uint32_t)max(K - (int)(chunk(NIP * wave + i) + ahead), 0);
     const bool gathered = g.row_to_slot != nullptr;
     qbase = gathered ? g.a : g.a + ((int64_t)t.seg0 + t.q0) * K;
     qbytes = gathered ? (uint32_t)(g.a_rows * K) : (uint32_t)t.qvalid * (uint32_t)K;
@@ -404,6 +418,8 @@ struct Loads {
       const int r = SPARE && q * 8 >= BQ ? -1 : src(row(q));
       voffQ[i] = r >= 0 ? (uint32_t)r * (uint32_t)K + chunk(q) : kOOB;
     }
+#pragma unroll
+    for (int i = 0; i < (NIQ == 1 ? 1 : 2); ++i) leftQ[i] = (uint32_t)max(K - (int)chunk(NIQ * wave + i), 0);
   }
   // one(i): instruction i of the stage at byte k0 of the rows, into the place
   // of the ring at `buf`
@@ -415,6 +431,14 @@ struct Loads {
     const uint32_t to = (isp ? ldsP : ldsQ) + buf + (uint32_t)j * 1024u;
     dma16(rs, SPARE && !isp && wave * 8 >= BQ ? spare : to,
           k0 < (isp ? leftP[j & 1] : leftQ[NIQ == 1 ? 0 : j & 1]) ? (isp ? voffP[isp ? j : 0] : voffQ[isp ? 0 : j]) : kOOB);
+  }
+  // stage -1: the first 64 bytes of the late rows, as the stage's second half
+  __device__ __forceinline__ void pre(const Fp8Args &g, uint32_t buf) const {
+    const bool on = late(g, pbase + (lane >> 3) * g.K);
+#pragma unroll
+    for (int i = 0; i < NIP; ++i)
+      dma16(make_rsrc(pbase, pbytes), ldsP + buf + (uint32_t)i * 1024u,
+            on && chunk(NIP * wave + i) >= 64u ? voffP[i] - 128u : kOOB);
   }
   __device__ __forceinline__ void issue(uint32_t k0, uint32_t buf) const {
 #pragma unroll
@@ -884,10 +908,10 @@ __global__ __launch_bounds__(512, 2) void k_grouped_fp8_wide(Fp8Args g) {
 // product: 28 against 30 us at 4 tokens, 49 against 53 at 16, 57 against 58 at
 // 64 (265 MB: 4.7 TB/s).  More rows want more work per byte loaded: 1024 rows,
 // 8 experts, 608 x 608: 9.1 and 9.4 us; 4096 rows: 15.7 and 11.8 us.
-template <bool GU, int BP, int NS, int NW>
+template <bool GU, int BP, int NS, int NW, bool LATE>
 __global__ __launch_bounds__(NW * 64) void k_grouped_fp8_small(Fp8Args g) {
   constexpr int BQ = 64, FP = BP / NW / 16, FQ = BQ / 16;
-  using L = Loads<GU, BP, BQ, NW>;
+  using L = Loads<GU, BP, BQ, NW, LATE>;
   static_assert(!GU || BP == 256, "a gate/up tile holds one block of 128 h");
   static_assert((NS - 2) * L::LOADS < 64, "vmcnt range");
   __shared__ u32x4_t smem[NS * (L::TP + L::TQ) + 64];
@@ -929,6 +953,8 @@ __global__ __launch_bounds__(NW * 64) void k_grouped_fp8_small(Fp8Args g) {
   };
   const int srow = src(lane);
   ld.tile(g, t, src);
+  // Loads: whether the lane's weight rows (lr and multiples of 16) are late
+  const bool late = L::late(g, ld.pbase + lr * g.K);
   auto load_scales = [&](int kc) {   // as in the wide kernel
     const int nd = min(kScaleChunk, cols - kc) >> 2;
     const u32x4_t rs =
@@ -945,6 +971,7 @@ __global__ __launch_bounds__(NW * 64) void k_grouped_fp8_small(Fp8Args g) {
     }
   };
   load_scales(0);
+  if (LATE) ld.pre(g, (NS - 1) * L::STAGE);
 #pragma unroll
   for (int n = 0; n < NS - 1; ++n) ld.issue(128u * n, n * L::STAGE);
   f32x4_t acc[FP][FQ];
@@ -954,6 +981,16 @@ __global__ __launch_bounds__(NW * 64) void k_grouped_fp8_small(Fp8Args g) {
     for (int j = 0; j < FQ; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   uint32_t buf = 0, last = (NS - 1) * L::STAGE;   // places of stage n and of stage n + NS - 1
   const int nlive = (t.qvalid + 15) >> 4;
+  auto half = [&](uint32_t at) { return *reinterpret_cast<const LDS_AS u32x4_t *>(lds + at); };
+  u32x4_t old[FP];   // second half of the last stage: of late rows, the first 64 k of this one
+  if constexpr (LATE) {
+    asm volatile("" ::: "memory");
+    wait_vm<(NS - 1) * L::LOADS>();
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < FP; ++i) old[i] = half((prow[i] * 128 + last + at0) ^ 64u);
+  }
   for (int n = 0; n < nk; ++n) {
     if (n > 0 && n % kScaleChunk == 0) {
       wait_lgkm();
@@ -972,7 +1009,11 @@ __global__ __launch_bounds__(NW * 64) void k_grouped_fp8_small(Fp8Args g) {
     uint32_t sp[FP];
 #pragma unroll
     for (int i = 0; i < FP; ++i) {
-      pf[i] = frag(lds + prow[i] * 128, buf + at0, 64u);
+      const uint32_t at = prow[i] * 128 + buf + at0;
+      const u32x4_t lo = half(at), hi = half(at ^ 64u);
+      const u32x4_t a = LATE && late ? old[i] : lo, b = LATE && late ? lo : hi;
+      old[i] = hi;
+      pf[i] = i32x8_t{(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
       sp[i] = s_ps[w][pblk[i]] >> sh;
     }
 #pragma unroll
@@ -1059,7 +1100,7 @@ __global__ __launch_bounds__(NW * 64) void k_grouped_fp8_small(Fp8Args g) {
 constexpr int64_t kFewRows = 32;
 constexpr int kCUs = 256;   // persistent kernels: one block of threads per CU, a multiple of 8
 
-template <bool GU, int BP, int NS, int NW>
+template <bool GU, int BP, int NS, int NW, bool LATE>
 int launch_small(Fp8Args g, int64_t active, const char *name, const char *fn, hipStream_t s) {
   constexpr int per = GU ? BP / 2 : BP;
   g.PT = (g.N + per - 1) / per;
@@ -1067,7 +1108,7 @@ int launch_small(Fp8Args g, int64_t active, const char *name, const char *fn, hi
   const int64_t tiles = (g.slots / 64 + active) * g.PT;
   MOE_REQUIRE(tiles < ((int64_t)1 << 30), MOE_ERR_UNSUPPORTED, "%s: too many tiles", fn);
   const unsigned blocks = (unsigned)((tiles + 7) / 8 * 8);
-  MOE_LAUNCH(name, s, (k_grouped_fp8_small<GU, BP, NS, NW><<<blocks, NW * 64, 0, s>>>(g)));
+  MOE_LAUNCH(name, s, (k_grouped_fp8_small<GU, BP, NS, NW, LATE><<<blocks, NW * 64, 0, s>>>(g)));
   return check_launch(fn);
 }
 
@@ -1075,7 +1116,11 @@ template <bool GU>
 int product(const Fp8Args &args, const char *name, const char *fn, hipStream_t s) {
   Fp8Args g = args;
   const int64_t active = g.E < g.slots ? (int64_t)g.E : g.slots;   // experts with rows, at most
-  if (g.slots <= kFewRows * active) return launch_small<GU, GU ? 256 : 64, GU ? 3 : 4, GU ? 8 : 4>(g, active, name, fn, s);
+  if (g.slots <= kFewRows * active) {
+    if constexpr (GU)
+      if (g.K % 128 == 64) return launch_small<GU, 256, 3, 8, true>(g, active, name, fn, s);
+    return launch_small<GU, GU ? 256 : 64, GU ? 3 : 4, GU ? 8 : 4, false>(g, active, name, fn, s);
+  }
   // Many rows, but so few small tiles (counting half a tile of 64 rows lost per
   // expert) that all run at once: gate/up one, else two blocks of threads to a
   // CU.  Event times against the wide kernel's: 608 x 608, 8 experts, 2048 rows
@@ -1084,7 +1129,7 @@ int product(const Fp8Args &args, const char *name, const char *fn, hipStream_t s
   // against 17.9; 1024 rows, 4 experts, 2880 x 2880 (414) 51 against 42 and 27
   // against 37; 2048 rows (782) 44 against 39.
   const int64_t small = (g.slots / 64 + active / 2) * ((g.N + 127) / 128);
-  if (small <= (GU ? kCUs : 2 * kCUs)) return launch_small<GU, GU ? 256 : 128, 3, 8>(g, active, name, fn, s);
+  if (small <= (GU ? kCUs : 2 * kCUs)) return launch_small<GU, GU ? 256 : 128, 3, 8, false>(g, active, name, fn, s);
   const int per = GU ? 128 : 256;
   g.PT = (g.N + per - 1) / per;
   const int64_t tiles = (g.slots / 256 + active) * g.PT;
