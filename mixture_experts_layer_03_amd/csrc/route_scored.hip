@@ -110,11 +110,30 @@ struct RouteArgs {
   int E, k;
   bool sigmoid, renorm, pairs;   // pairs: a group's value is the sum of its two best
   int groups, keep, size;        // groups that compete (1: no restriction), kept, experts each
-  int span;                      // lanes per group, a power of two
+  int span, span_log;            // lanes per group, a power of two
   float scale;
   int32_t *idx;
   float *w;
 };
+
+// The lane's V values of a group's, `none` where it has no expert.
+typedef float f32x4u_t __attribute__((ext_vector_type(4), aligned(4)));
+template <int V>
+__device__ __forceinline__ void load(const RouteArgs &g, const float *p, bool in, int li, float none,
+                                     float (&c)[V]) {
+  if (V % 4 == 0 && g.size % 4 == 0) {   // four or none of four
+#pragma unroll
+    for (int v = 0; v < V; v += 4) {
+      f32x4u_t r = {none, none, none, none};
+      if (in && li * V + v < g.size) r = *reinterpret_cast<const f32x4u_t *>(p + li * V + v);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) c[(v + i) % V] = r[i];
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v) c[v] = in && li * V + v < g.size ? p[li * V + v] : none;
+  }
+}
 
 // The lane's choices in fp64 (0 where it has no expert), and as a mask where
 // it has one; ranked: what the groups compare.
@@ -127,7 +146,7 @@ __device__ __forceinline__ unsigned choices64(const RouteArgs &g, const float *x
     double sum = 0.0;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int o = v * g.span + li;
+      const int o = li * V + v;
       if (gi < g.groups && o < g.size) sum += exp((double)x[base + o] - (double)shift);
     }
     for (int m = 1; m < G; m <<= 1) sum += __shfl_xor(sum, m, 64);
@@ -137,7 +156,7 @@ __device__ __forceinline__ unsigned choices64(const RouteArgs &g, const float *x
   first = second = kLowest;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int o = v * g.span + li;
+    const int o = li * V + v;
     c[v] = 0.0;
     if (gi >= g.groups || o >= g.size) continue;
     const double xe = x[base + o];
@@ -186,7 +205,7 @@ __device__ __forceinline__ int select64(const RouteArgs &g, const float *x, int 
     int bi = 0x7fffffff;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int e = base + v * g.span + li;
+      const int e = base + li * V + v;
       if (((open >> v) & 1) && (bi == 0x7fffffff || ranks_before(c[v], e, bv, bi))) {
         bv = c[v];
         bi = e;
@@ -201,14 +220,15 @@ __device__ __forceinline__ int select64(const RouteArgs &g, const float *x, int 
         bi = oi;
       }
     }
-    if (own == bi && bi != 0x7fffffff) open &= ~(1u << ((bi - base) / g.span));
+    if (own == bi && bi != 0x7fffffff) open &= ~(1u << (bi - base - li * V));
     if (s == j) mine = bi;
   }
   return mine;
 }
 
 // G lanes per token, V experts per lane: lane s holds experts size * (s / span)
-// + span * v + s % span, so that a group's experts lie in span adjacent lanes.
+// + V (s % span) + v, so that a group's experts lie in span adjacent lanes and
+// are read 16 bytes at a time.
 //
 // Quick form, in fp32: the group values, then k rounds of a maximum over the
 // lane's V values and the G lanes (one instruction per step), the winner
@@ -224,20 +244,21 @@ __device__ __forceinline__ int select64(const RouteArgs &g, const float *x, int 
 // the order are, the first k + 1 are ranked again in fp64; where that cannot
 // settle it (the k + 2nd is close too, a NaN, scores of -inf), the wave
 // selects in fp64 from the start.
+//
+// The vector units bound it, not memory: 32768 tokens x 256 experts in 8
+// groups, sigmoid, bias, top-8 take 22 us (31 at V = 4, 24 at V = 16; the
+// logits' 34 MB alone 7), about 750 instructions per two tokens, of which a
+// round is 37.
 template <int G, int V>
 __global__ __launch_bounds__(256) void k_route_scored(RouteArgs g) {
   __shared__ int2 s_place[256 / G][G];   // the selected experts and their keys, and the next
   const int s = threadIdx.x % G;
   const int64_t t = ((int64_t)blockIdx.x * 256 + threadIdx.x) / G;
   const bool live = t < g.T;
-  const int li = s % g.span, gi = s / g.span, base = gi * g.size;
+  const int gi = s >> g.span_log, li = s - (gi << g.span_log), base = gi * g.size;
   const float *x = g.logits + (live ? t : 0) * g.E;
   float c[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int o = v * g.span + li;
-    c[v] = gi < g.groups && o < g.size ? x[base + o] : kLowest;
-  }
+  load<V>(g, x + base, gi < g.groups, li, kLowest, c);
   bool unsure = false;
   float shift = 0.0f, sum = 0.0f, top = 1.0f;
   const bool scored = g.bias || (g.pairs && g.keep < g.groups);   // scores are compared
@@ -252,31 +273,45 @@ __global__ __launch_bounds__(256) void k_route_scored(RouteArgs g) {
     sum = reduce<G>(sum, Add());
     top = sum == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(sum);   // the largest score
   }
-  auto score = [&](float v) {
-    return g.sigmoid ? __builtin_amdgcn_rcpf(1.0f + __expf(-v)) : __expf(v - shift) * top;
-  };
+  auto sigmoid = [](float v) { return __builtin_amdgcn_rcpf(1.0f + __expf(-v)); };
   // what two compared values may be off together
   const float tol = g.sigmoid ? 0x1p-20f : 0x1p-23f * (2.0f + 40.0f * top);
   auto slack = [&](float v) { return tol + 0x1p-22f * fabsf(v); };
+  float r[V];
+  if (g.bias) {   // (no expert: 0 - infinity)
+    load<V>(g, g.bias + base, gi < g.groups, li, kLowest, r);
+    if (g.sigmoid) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) r[v] += sigmoid(c[v]);
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) r[v] += __expf(c[v] - shift) * top;
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v) r[v] = c[v];
+  }
   int key[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int o = v * g.span + li;
-    const bool in = gi < g.groups && o < g.size;
-    float r = c[v];
-    if (g.bias) r = in ? score(r) + g.bias[base + o] : kLowest;
-    unsure |= r != r;
-    key[v] = to_key(r + 0.0f);
+    unsure |= r[v] != r[v];
+    key[v] = to_key(r[v] + 0.0f);
   }
   if (g.keep < g.groups) {
     int a = kLowestKey, b = kLowestKey;
+    auto take = [&](int k) {
+      b = max(b, min(a, k));
+      a = max(a, k);
+    };
+    if (g.pairs && !g.bias) {   // the scores' sum; a score of no expert would be 0
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int o = v * g.span + li;
-      int r = key[v];
-      if (g.pairs && !g.bias) r = gi < g.groups && o < g.size ? to_key(score(c[v])) : kLowestKey;
-      b = max(b, min(a, r));
-      a = max(a, r);
+      for (int v = 0; v < V; ++v) {
+        const int k = to_key(g.sigmoid ? sigmoid(c[v]) : __expf(c[v] - shift) * top);
+        take(gi < g.groups && li * V + v < g.size ? k : kLowestKey);
+      }
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) take(key[v]);
     }
     top2(a, b, g.span);
     const float val = g.pairs ? from_key(a) + from_key(b) : from_key(a);
@@ -316,7 +351,7 @@ __global__ __launch_bounds__(256) void k_route_scored(RouteArgs g) {
       int at = 0;
 #pragma unroll
       for (int v = V - 1; v >= 0; --v) at = key[v] == best ? v : at;
-      const int e = base + at * g.span + li;
+      const int e = base + li * V + at;
       const int low = reduce<G>(has ? e : 0x7fffffff, Min());
       has = has && e == low;
     }
@@ -330,7 +365,7 @@ __global__ __launch_bounds__(256) void k_route_scored(RouteArgs g) {
       key[v] = hit ? kLowestKey : key[v];
       rest = rest && !hit;
     }
-    if (has) place[j] = int2{base + at * g.span + li, best};
+    if (has) place[j] = int2{base + li * V + at, best};
   }
   // (a token's lanes are lanes of one wave, whose LDS operations keep their order)
   asm volatile("" ::: "memory");
@@ -546,6 +581,7 @@ extern "C" int moe_route_scored(const float *logits, const float *sel_bias, int6
   while (G < k + (sel_bias ? 1 : 0) || G < span2) G <<= 1;
   while (G < 64 && (g.size + G / span2 - 1) / (G / span2) > want) G <<= 1;
   g.span = G / span2;
+  while (1 << g.span_log < g.span) ++g.span_log;
   while (V * g.span < g.size) V <<= 1;
   const unsigned blocks = (unsigned)((T * G + 255) / 256);
 #define ROUTE_CASE(GV, VV)                                                                        \
