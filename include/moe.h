@@ -468,12 +468,12 @@ int moe_aux_loss(const float *logits, const int32_t *load, int64_t T, int64_t n_
  * below every number (in a group's value it counts as -inf).  topk_idx is in
  * descending order of c_e.  Logits of -inf (masked experts) have score 0;
  * with renorm, a selection of scores that are all 0 gets weights 0 (scores
- * too small for fp32 still share the weight in proportion).  A NaN logit makes its own sigmoid score,
- * or all softmax scores of its row, NaN, and +inf the softmax scores of its
- * row; with renorm only what is selected matters.  sel_bias must be finite.
+ * too small for fp32 still share the weight in proportion).  A NaN logit makes
+ * its own sigmoid score, or all softmax scores of its row, NaN, and +inf the
+ * softmax scores of its row; with renorm only what is selected matters.  sel_bias must be finite.
  * 1 <= n_group <= 32 and a divisor of E; group_top 2 needs groups of two
  * experts or more; k <= topk_group * E / n_group; scale positive and finite;
- * T * k < 2^31; logits 16-byte aligned.  Outputs as moe_route's.
+ * T < 2^26; logits 16-byte aligned.  Outputs as moe_route's.
  */
 #define MOE_SCORE_SOFTMAX 0
 #define MOE_SCORE_SIGMOID 1

@@ -524,7 +524,8 @@ int check_scored(const char *fn, int64_t T, int E, int k, int score, float scale
   MOE_REQUIRE(E >= 1 && E <= kMaxExperts, MOE_ERR_UNSUPPORTED, "%s: E=%d outside [1,%d]", fn, E,
               kMaxExperts);
   MOE_REQUIRE(k >= 1 && k <= E && k <= kMaxTopK, MOE_ERR_UNSUPPORTED, "%s: k=%d E=%d", fn, k, E);
-  MOE_REQUIRE(T * k < ((int64_t)1 << 31), MOE_ERR_UNSUPPORTED, "%s: T*k >= 2^31", fn);
+  // (a launch has at most 2^32 threads, a token up to 64)
+  MOE_REQUIRE(T < ((int64_t)1 << 26), MOE_ERR_UNSUPPORTED, "%s: T >= 2^26", fn);
   MOE_REQUIRE(score == MOE_SCORE_SOFTMAX || score == MOE_SCORE_SIGMOID, MOE_ERR_UNSUPPORTED,
               "%s: score %d", fn, score);
   MOE_REQUIRE(scale > 0.0f && scale <= 3.402823466e38f, MOE_ERR_INVALID_ARG,

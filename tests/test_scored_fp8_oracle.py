@@ -171,3 +171,10 @@ def test_products_refuse():
         a[i] = v
         assert L.moe_grouped_ffn_fwd_fp8(*a) == rc, (i, v)
     assert L.moe_grouped_ffn_fwd_fp8(*([None] * 3 + [0, None, 8, 0, 64, 64] + [None] * 9)) == 0
+
+
+def test_more_tokens_than_a_launch_has_threads_for_are_refused():
+    L = abi.lib()
+    f = ctypes.c_float(1.0)
+    assert _route(L, T=1 << 26, k=1) == -2
+    assert L.moe_route_scored_bwd(P, P, P, P, P, 1 << 26, 16, 1, 1, 1, f, P, P, None) == -2
