@@ -91,32 +91,32 @@ __global__ __launch_bounds__(256) void k_quant_rows(const T *__restrict__ x, int
                                                     uint8_t *__restrict__ q,
                                                     uint8_t *__restrict__ scale, int steps) {
   const int lane = threadIdx.x & 63;
-  const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (r >= R) return;
   const int nb = scale_blocks(K), cols = scale_cols(K);
-  const T *row = x + r * K;
   const int first = (int)blockIdx.y * steps * 4, end = min(first + steps * 4, cols);
-  for (int b0 = first; b0 < end; b0 += 4) {
-    const int blk = b0 + (lane >> 4), c = blk * kBlk + (lane & 15) * 8;
-    float v[8];
+  for (int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); r < R; r += (int64_t)gridDim.x * 4) {
+    const T *row = x + r * K;
+    for (int b0 = first; b0 < end; b0 += 4) {
+      const int blk = b0 + (lane >> 4), c = blk * kBlk + (lane & 15) * 8;
+      float v[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-    if (c < K) load8(row + c, v);
-    float m = 0.0f;
+      for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+      if (c < K) load8(row + c, v);
+      float m = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, finite_abs(v[i]));
+      for (int i = 0; i < 8; ++i) m = fmaxf(m, finite_abs(v[i]));
 #pragma unroll
-    for (int s = 1; s < 16; s <<= 1) m = fmaxf(m, __shfl_xor(m, s, 64));
-    const uint32_t byte = blk < nb ? scale_byte(m) : 127u;
-    const float inv = inv_scale(byte);
-    if (c < K) {
-      float w[8];
+      for (int s = 1; s < 16; s <<= 1) m = fmaxf(m, __shfl_xor(m, s, 64));
+      const uint32_t byte = blk < nb ? scale_byte(m) : 127u;
+      const float inv = inv_scale(byte);
+      if (c < K) {
+        float w[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = scaled(v[i], inv);
-      *reinterpret_cast<u32x2_t *>(q + r * K + c) =
-          u32x2_t{pack_e4m3x4(w[0], w[1], w[2], w[3]), pack_e4m3x4(w[4], w[5], w[6], w[7])};
+        for (int i = 0; i < 8; ++i) w[i] = scaled(v[i], inv);
+        *reinterpret_cast<u32x2_t *>(q + r * K + c) =
+            u32x2_t{pack_e4m3x4(w[0], w[1], w[2], w[3]), pack_e4m3x4(w[4], w[5], w[6], w[7])};
+      }
+      if ((lane & 15) == 0) scale[r * cols + blk] = (uint8_t)byte;
     }
-    if ((lane & 15) == 0) scale[r * cols + blk] = (uint8_t)byte;
   }
 }
 
@@ -292,6 +292,10 @@ struct Tile {
 struct Tiles {
   int off[kMaxExperts + 1];     // the experts' first rows, in [0, R]
   int start[kMaxExperts + 1];   // the experts' first tiles
+  template <int BQ>
+  static __device__ __forceinline__ int row_tiles(int rows) {
+    return rows / BQ + (rows % BQ != 0);
+  }
   // by all threads of the block
   template <int BQ>
   __device__ __forceinline__ void init(const Fp8Args &g) {
@@ -303,14 +307,16 @@ struct Tiles {
       int base = 0;
       for (int e0 = 0; e0 < g.E; e0 += 64) {
         const int e = e0 + lane;
-        int n = e < g.E ? (max(off[e + 1] - off[e], 0) + BQ - 1) / BQ * g.PT : 0;
+        // (offsets that go up and down could add up to more: sums stop at 2^30)
+        uint32_t n = e < g.E ? (uint32_t)(row_tiles<BQ>(max(off[e + 1] - off[e], 0)) * g.PT) : 0u;
 #pragma unroll
         for (int m = 1; m < 64; m <<= 1) {
-          const int o = __shfl_up(n, m, 64);
-          if (lane >= m) n += o;
+          const uint32_t o = (uint32_t)__shfl_up((int)n, m, 64);
+          if (lane >= m) n = min(n + o, 1u << 30);
         }
-        if (e < g.E) start[e + 1] = base + n;
-        base += __builtin_amdgcn_readlane(n, 63);
+        n = min(n + (uint32_t)base, 1u << 30);
+        if (e < g.E) start[e + 1] = (int)n;
+        base = __builtin_amdgcn_readlane((int)n, 63);
       }
       if (lane == 0) start[0] = 0;
     }
@@ -329,7 +335,7 @@ struct Tiles {
         t.e = __builtin_amdgcn_readfirstlane(e0 + __ffsll((unsigned long long)hit) - 1);
         t.seg0 = __builtin_amdgcn_readfirstlane(off[t.e]);
         const int rows = __builtin_amdgcn_readfirstlane(off[t.e + 1]) - t.seg0;
-        const int qt = (rows + BQ - 1) / BQ;
+        const int qt = row_tiles<BQ>(rows);
         const int in = at - __builtin_amdgcn_readfirstlane(start[t.e]);
         t.pt = in / qt;
         t.q0 = (in % qt) * BQ;
@@ -1187,7 +1193,7 @@ extern "C" int moe_quant_rows_fp8(const void *x, int dtype, int64_t R, int K, ui
               "%s: pointers must be 16-byte aligned", fn);
   hipStream_t s = (hipStream_t)stream;
   const int steps = R < kCUs * 16 ? 1 : scale_cols(K) / 4;
-  const dim3 blocks((unsigned)((R + 3) / 4), (unsigned)(scale_cols(K) / 4 / steps));
+  const dim3 blocks((unsigned)min((R + 3) / 4, (int64_t)1 << 22), (unsigned)(scale_cols(K) / 4 / steps));
   if (dtype == MOE_BF16)
     MOE_LAUNCH("quant_rows_fp8", s,
                k_quant_rows<bf16_t><<<blocks, 256, 0, s>>>((const bf16_t *)x, R, K, q, scale,

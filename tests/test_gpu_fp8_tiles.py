@@ -131,3 +131,133 @@ def test_quant_rows_where_the_split_over_waves_ends(R):
     torch.cuda.synchronize()
     rq, rs = S.quant_rows(x)
     assert np.array_equal(sc.cpu().numpy(), rs) and np.array_equal(q.cpu().numpy(), rq)
+
+
+@pytest.mark.parametrize("shift", [16, 64, 112])
+@pytest.mark.parametrize("counts,d,f", [([3, 0, 20], 192, 144), ([600], 144, 4112), ([90, 70], 576, 272)],
+                         ids=["few", "big", "mid"])
+def test_pointers_aligned_to_16_bytes_only(counts, d, f, shift):
+    """The results do not depend on where in a line the operands begin."""
+    import torch
+    from mixture_experts_layer_03_amd import abi
+    dev = need_gpu()
+    r = _rng(d + f)
+    E, R = len(counts), sum(counts)
+
+    def at(t):   # the same bytes, `shift` behind a line
+        raw = t.contiguous().view(torch.uint8).reshape(-1)
+        buf = torch.zeros(raw.numel() + 128 + shift, dtype=torch.uint8, device=dev)
+        base = -buf.data_ptr() % 128 + shift
+        buf[base:base + raw.numel()] = raw
+        return buf[base:base + raw.numel()].view(t.dtype).view(t.shape)
+
+    x = torch.from_numpy(r.standard_normal((R, d)).astype(np.float32)).to(dev).bfloat16()
+    wg = torch.from_numpy(r.standard_normal((E, 2 * f, d)).astype(np.float32)).to(dev)
+    wd = torch.from_numpy(r.standard_normal((E, d, f)).astype(np.float32)).to(dev)
+    off = _i32(_offsets(counts), dev)
+    out = []
+    for put in (lambda t: t, at):
+        u8 = dict(dtype=torch.uint8, device=dev)
+        q, s = put(torch.zeros(R, d, **u8)), put(torch.zeros(R, S.scale_cols(d), **u8))
+        abi.moe_quant_rows_fp8(put(x), q, s)
+        gq, gs = put(torch.zeros(E, 2 * f, d, **u8)), put(torch.zeros(E, -(-2 * f // 128), S.scale_cols(d), **u8))
+        abi.moe_quant_weights_fp8(put(wg), gq, gs)
+        dq, ds = put(torch.zeros(E, d, f, **u8)), put(torch.zeros(E, -(-d // 128), S.scale_cols(f), **u8))
+        dt, dts = put(torch.zeros(E, f, d, **u8)), put(torch.zeros(E, -(-f // 128), S.scale_cols(d), **u8))
+        abi.moe_quant_weights_fp8(put(wd), dq, ds, dt, dts)
+        h, hs = put(torch.zeros(R, f, **u8)), put(torch.zeros(R, S.scale_cols(f), **u8))
+        y = put(torch.zeros(R, d, dtype=torch.bfloat16, device=dev))
+        abi.moe_grouped_ffn_fwd_fp8(q, s, off, gq, gs, dq, ds, None, h, hs, y)
+        torch.cuda.synchronize()
+        out.append([q, s, gq, gs, dq, ds, dt, dts, h, hs, y])
+    for a, b in zip(*out):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+def _whole(gen, *shape):
+    """Whole numbers up to 8 as e4m3, drawn a slice at a time."""
+    import torch
+    out = torch.empty(shape, dtype=torch.float8_e4m3fn, device=gen.device)
+    for i in range(shape[0]):
+        out[i] = torch.randint(-8, 9, shape[1:], generator=gen, device=gen.device).to(torch.float8_e4m3fn)
+    return out
+
+
+def test_results_past_2_31_elements():
+    import torch
+    from mixture_experts_layer_03_amd import abi
+    dev = need_gpu()
+    gen = torch.Generator(device=dev).manual_seed(1)
+    R, N, K, E = 70000, 32768, 64, 3
+    a, b = _whole(gen, 1, R, K)[0], _whole(gen, E, N, K)
+    one = dict(fill_value=127, dtype=torch.uint8, device=dev)
+    asc, bsc = torch.full((R, 4), **one), torch.full((E, N // 128, 4), **one)
+    off = [0, 1000, 69000, R]
+    c = torch.empty(R, N, dtype=torch.bfloat16, device=dev)
+    assert c.numel() > 2 ** 31
+    abi.moe_grouped_gemm_fp8(a, asc, _i32(off, dev), b, bsc, None, c)
+    torch.cuda.synchronize()
+    for e, rows in enumerate([slice(0, 64), slice(65500, 65600), slice(R - 200, R)]):
+        assert torch.equal(c[rows], (a[rows].float() @ b[e].float().T).bfloat16()), e   # exact, rounded once
+
+
+@pytest.mark.parametrize("rows", [2, 40], ids=["few", "big"])
+def test_weights_past_2_31_bytes(rows):
+    import torch
+    from mixture_experts_layer_03_amd import abi
+    dev = need_gpu()
+    gen = torch.Generator(device=dev).manual_seed(rows)
+    E, N, K = 520, 2048, 2064
+    R = E * rows
+    a, b = _whole(gen, 1, R, K)[0], _whole(gen, E, N, K)
+    assert b.numel() > 2 ** 31
+    one = dict(fill_value=127, dtype=torch.uint8, device=dev)
+    asc, bsc = torch.full((R, S.scale_cols(K)), **one), torch.full((E, N // 128, S.scale_cols(K)), **one)
+    off = _i32(np.arange(E + 1) * rows, dev)
+    c = torch.empty(R, N, dtype=torch.bfloat16, device=dev)
+    abi.moe_grouped_gemm_fp8(a, asc, off, b, bsc, None, c)
+    torch.cuda.synchronize()
+    for e in (0, 259, 508, 519):
+        i = slice(e * rows, (e + 1) * rows)
+        assert torch.equal(c[i], (a[i].float() @ b[e].float().T).bfloat16()), e
+    if rows > 2:
+        return
+    # gate/up over the same bytes: the last expert's rows by themselves give the same
+    f, i = N // 2, slice(R - 2, R)
+    dq, ds = _whole(gen, E, K, f), torch.full((E, -(-K // 128), S.scale_cols(f)), **one)
+
+    def ffn(x, xs, o, e):
+        n = x.shape[0]
+        h, hs = torch.empty(n, f, dtype=torch.uint8, device=dev), torch.empty(n, S.scale_cols(f), dtype=torch.uint8, device=dev)
+        y = torch.empty(n, K, dtype=torch.bfloat16, device=dev)
+        abi.moe_grouped_ffn_fwd_fp8(x, xs, o, b[e], bsc[e].clone(), dq[e], ds[e].clone(), None, h, hs, y)
+        torch.cuda.synchronize()
+        return h, hs, y
+    whole, last = ffn(a, asc, off, slice(0, E)), ffn(a[i].clone(), asc[i].clone(), _i32([0, 2], dev), slice(E - 1, E))
+    for p, q in zip(whole, last):
+        assert torch.equal(p[i], q)
+
+
+def test_quantisation_past_2_31_elements():
+    import torch
+    from mixture_experts_layer_03_amd import abi
+    dev = need_gpu()
+    u8 = dict(dtype=torch.uint8, device=dev)
+    x = torch.empty(300000, 8192, dtype=torch.bfloat16, device=dev).normal_()
+    assert x.numel() > 2 ** 31
+    q, s = torch.empty(x.shape, **u8), torch.empty(x.shape[0], 64, **u8)
+    abi.moe_quant_rows_fp8(x, q, s)
+    lq, ls = torch.empty(50, 8192, **u8), torch.empty(50, 64, **u8)
+    abi.moe_quant_rows_fp8(x[-50:], lq, ls)
+    torch.cuda.synchronize()
+    assert torch.equal(q[-50:], lq) and torch.equal(s[-50:], ls)
+    w = x.view(-1)[:600 * 2048 * 1936].view(600, 2048, 1936)
+    sizes = [(2048, 1936), (16, 16), (1936, 2048), (16, 16)]
+    out = [torch.empty(600, *z, **u8) for z in sizes]
+    assert S.scale_cols(1936) == S.scale_cols(2048) == 16 and out[0].numel() > 2 ** 31
+    abi.moe_quant_weights_fp8(w, *out)
+    last = [torch.empty(1, *z, **u8) for z in sizes]
+    abi.moe_quant_weights_fp8(w[-1:], *last)
+    torch.cuda.synchronize()
+    for p, q in zip(out, last):
+        assert torch.equal(p[-1:], q)
