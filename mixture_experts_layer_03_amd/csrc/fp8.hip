@@ -289,56 +289,58 @@ struct Tile {
 // Tiles are numbered expert, then output columns, then rows (fastest), BQ rows
 // each, and split into 8 contiguous chunks, one per XCD (blocks go round the
 // XCDs): the tiles in flight on an XCD share their weight slab in its L2.
+// KINDS = 2: an expert's last tile, if it has half the rows or fewer, is of
+// the second kind, which has numbers and chunks of its own.
+template <int BQ, int KINDS>
 struct Tiles {
-  int off[kMaxExperts + 1];     // the experts' first rows, in [0, R]
-  int start[kMaxExperts + 1];   // the experts' first tiles
-  template <int BQ>
-  static __device__ __forceinline__ int row_tiles(int rows) {
-    return rows / BQ + (rows % BQ != 0);
+  int off[kMaxExperts + 1];            // the experts' first rows, in [0, R]
+  int start[KINDS][kMaxExperts + 1];   // the experts' first tiles
+  static __device__ __forceinline__ int row_tiles(int rows, int kind) {
+    const int rest = rows % BQ;
+    if (KINDS == 1) return rows / BQ + (rest != 0);
+    return kind == 0 ? rows / BQ + (rest > BQ / 2) : rest > 0 && rest <= BQ / 2;
   }
   // by all threads of the block
-  template <int BQ>
   __device__ __forceinline__ void init(const Fp8Args &g) {
-    const int lane = threadIdx.x & 63;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     for (int i = threadIdx.x; i <= g.E; i += blockDim.x)
       off[i] = (int)min(max((int64_t)g.offsets[i], (int64_t)0), g.slots);
     __syncthreads();
-    if (threadIdx.x < 64) {
+    if (wave < KINDS) {
       int base = 0;
       for (int e0 = 0; e0 < g.E; e0 += 64) {
         const int e = e0 + lane;
         // (offsets that go up and down could add up to more: sums stop at 2^30)
-        uint32_t n = e < g.E ? (uint32_t)(row_tiles<BQ>(max(off[e + 1] - off[e], 0)) * g.PT) : 0u;
+        uint32_t n = e < g.E ? (uint32_t)(row_tiles(max(off[e + 1] - off[e], 0), wave) * g.PT) : 0u;
 #pragma unroll
         for (int m = 1; m < 64; m <<= 1) {
           const uint32_t o = (uint32_t)__shfl_up((int)n, m, 64);
           if (lane >= m) n = min(n + o, 1u << 30);
         }
         n = min(n + (uint32_t)base, 1u << 30);
-        if (e < g.E) start[e + 1] = (int)n;
+        if (e < g.E) start[wave][e + 1] = (int)n;
         base = __builtin_amdgcn_readlane((int)n, 63);
       }
-      if (lane == 0) start[0] = 0;
+      if (lane == 0) start[wave][0] = 0;
     }
     __syncthreads();
   }
-  __device__ __forceinline__ int total(const Fp8Args &g) const {
-    return __builtin_amdgcn_readfirstlane(start[g.E]);
+  __device__ __forceinline__ int total(const Fp8Args &g, int kind) const {
+    return __builtin_amdgcn_readfirstlane(start[kind][g.E]);
   }
-  template <int BQ>
-  __device__ __forceinline__ Tile decode(const Fp8Args &g, int at) const {
+  __device__ __forceinline__ Tile decode(const Fp8Args &g, int kind, int at) const {
     const int lane = threadIdx.x & 63;
     for (int e0 = 0;; e0 += 64) {
-      const uint64_t hit = __ballot(e0 + lane < g.E && start[min(e0 + lane, g.E - 1) + 1] > at);
+      const uint64_t hit = __ballot(e0 + lane < g.E && start[kind][min(e0 + lane, g.E - 1) + 1] > at);
       if (hit) {
         Tile t;
         t.e = __builtin_amdgcn_readfirstlane(e0 + __ffsll((unsigned long long)hit) - 1);
         t.seg0 = __builtin_amdgcn_readfirstlane(off[t.e]);
         const int rows = __builtin_amdgcn_readfirstlane(off[t.e + 1]) - t.seg0;
-        const int qt = row_tiles<BQ>(rows);
-        const int in = at - __builtin_amdgcn_readfirstlane(start[t.e]);
+        const int qt = row_tiles(rows, kind);
+        const int in = at - __builtin_amdgcn_readfirstlane(start[kind][t.e]);
         t.pt = in / qt;
-        t.q0 = (in % qt) * BQ;
+        t.q0 = kind ? rows / BQ * BQ : (in % qt) * BQ;
         t.qvalid = min(rows - t.q0, BQ);
         return t;
       }
@@ -525,6 +527,11 @@ struct WideLoads {
     dma16(make_rsrc(qbase + k0, max(qbytes, k0) - k0), ldsQ + buf + (uint32_t)i * 1024u,
           k0 < left[i & 1] ? voffQ[i] : kOOB);
   }
+  // all offsets in registers here
+  __device__ __forceinline__ void keep() {
+    asm volatile("" : "+v"(voffP[0]), "+v"(voffP[1]), "+v"(voffQ[0]), "+v"(voffQ[1]), "+v"(voffQ[2]),
+                 "+v"(voffQ[3]), "+v"(left[0]), "+v"(left[1]));
+  }
   // Q rows and P half 0 (6 instructions), then P half 1 (2)
   __device__ __forceinline__ void front(int i, uint32_t k0, uint32_t buf) const {
     if (i < 4) q(i, k0, buf);
@@ -554,22 +561,27 @@ struct WideLoads {
 // first stage and scales are loaded while the epilogue runs, which uses the
 // ring's other place.
 //
-// 16384 rows x 32 experts, d = f = 2880: gate/up 545 GFLOP in 362 us, down 272
-// GFLOP in 198 us.  With the MFMAs taken out 251 us, with the loads taken out
-// 270 us (gate/up): neither alone bounds, and the clock falls under both.  One
-// barrier a stage, with loads one stage ahead, took 379 and 204 us; big and
-// small tiles dealt out separately, so that no CU gets one big tile more than
-// another, took longer (an expert's slab is then fetched twice).
+// 16384 rows x 32 experts, d = f = 2880: gate/up 545 GFLOP in 340 to 355 us
+// (as cards differ), down 272 GFLOP in 185 to 190 us; 16384 x 2880 x 5760 over
+// 8 experts of 2048 rows 223 to 237 us (2.4 PFLOP/s), over 32 of 512 rows 255
+// to 262.  With the MFMAs taken out 251 us, with the loads taken out 270 us
+// (gate/up): neither alone bounds, and half of the lines come from beyond the
+// XCD's L2.  Where experts have a few rows more than a multiple of 256, their
+// last tiles read all their weight rows again: experts of 479 to 558 rows take
+// 330 us (350 with big and small tiles dealt out as one).  Tried: one barrier
+// a stage with loads one stage ahead (379 and 204 us for the FFN's products),
+// 4 waves of 128 x 128 with half the LDS reads and 512 registers (gate/up as
+// fast, down 224 us: one wave per SIMD hides neither epilogue nor waits).
 template <bool GU>
 __global__ __launch_bounds__(512, 2) void k_grouped_fp8_wide(Fp8Args g) {
-  constexpr int BP = 256, BQ = 256, WP = 2, NW = 8, FP = 4, FQ = 2;
+  constexpr int BP = 256, BQ = 256, WP = 2, NW = 8, FP = 4, FQ = 2, NSP = GU ? 3 : 2;
   using L = WideLoads<GU>;
   __shared__ u32x4_t smem[2 * L::STAGE / 16];
   __shared__ uint32_t s_qs[kScaleChunk / 4][BQ];   // scales of a chunk of K blocks, four to a dword
   __shared__ uint32_t s_ps[kScaleChunk / 4][4];
   __shared__ int s_slot[BQ];                        // gathered rows: the next tile's slots
   __shared__ float s_amax[GU ? WP : 1][GU ? BQ : 1];
-  __shared__ Tiles tiles;
+  __shared__ Tiles<BQ, 2> tiles;
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -577,12 +589,40 @@ __global__ __launch_bounds__(512, 2) void k_grouped_fp8_wide(Fp8Args g) {
   const int N = g.N, nk = scale_blocks(g.K), cols = scale_cols(g.K);
   const bool gathered = g.row_to_slot != nullptr;
 
-  tiles.template init<BQ>(g);
-  const int total = tiles.total(g);
-  const int per = (int)(gridDim.x >> 3), chunk = (total + 7) >> 3;
-  const int cend = min(total, ((int)(blockIdx.x & 7) + 1) * chunk);
-  int id = (int)(blockIdx.x & 7) * chunk + (int)(blockIdx.x >> 3);
-  if (id >= cend) return;
+  // The blocks of an XCD take its big tiles in turn, and its small ones in turn
+  // from where the big ones ended, so that none gets one big tile more while
+  // another has a small one left; a block works through both in the order of
+  // the experts.
+  tiles.init(g);
+  const int per = (int)(gridDim.x >> 3);
+  int at[2], last[2];   // the block's next tile of each kind, and the end of its XCD's
+  {
+    int first = (int)(blockIdx.x >> 3);
+#pragma unroll
+    for (int kind = 0; kind < 2; ++kind) {
+      const int total = tiles.total(g, kind), chunk = (total + 7) >> 3, from = (int)(blockIdx.x & 7) * chunk;
+      last[kind] = min(total, from + chunk);
+      at[kind] = from + first;
+      first -= max(last[kind] - from, 0) % per;
+      if (first < 0) first += per;
+    }
+  }
+  // the block's next tile; e = E after the last
+  auto take = [&]() -> Tile {
+    Tile t{g.E, 0, 0, 0, 0};
+    bool small = false;
+    if (at[0] < last[0]) t = tiles.decode(g, 0, at[0]);
+    if (at[1] < last[1]) {
+      const Tile u = tiles.decode(g, 1, at[1]);
+      if (u.e < t.e || (u.e == t.e && u.pt < t.pt)) {
+        t = u;
+        small = true;
+      }
+    }
+    at[0] += small ? 0 : per;
+    at[1] += small ? per : 0;
+    return t;
+  };
 
   // ---- loads of a tile: its slots, its scales of a chunk of K blocks
   L ld;
@@ -637,7 +677,8 @@ __global__ __launch_bounds__(512, 2) void k_grouped_fp8_wide(Fp8Args g) {
   // lane's first chunk of the first 64 k: row lr, chunk lg; of the others:
   // chunk bit 2; the fragment's second chunk: bit 1
   const uint32_t at0 = (uint32_t)lr * 128u + (uint32_t)((lg ^ ((lr >> 1) & 7)) * 16);
-  Tile t = tiles.template decode<BQ>(g, id);
+  Tile t = take();
+  if (t.e >= g.E) return;
   if (gathered) load_slots(t);
   wait_vm<0>();
   __syncthreads();
@@ -646,10 +687,8 @@ __global__ __launch_bounds__(512, 2) void k_grouped_fp8_wide(Fp8Args g) {
   load_scales(t, 0);
   wait_vm<0>();
   for (;;) {
-    const int next = id + per;
-    const bool more = next < cend;
-    Tile tn = t;
-    if (more) tn = tiles.template decode<BQ>(g, next);
+    const Tile tn = take();
+    const bool more = tn.e < g.E;
     f32x16_t acc[FP][FQ];
 #pragma unroll
     for (int i = 0; i < FP; ++i)
@@ -658,14 +697,21 @@ __global__ __launch_bounds__(512, 2) void k_grouped_fp8_wide(Fp8Args g) {
 #pragma unroll
         for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
     const int p0 = t.pt * (GU ? BP / 2 : BP);
-    int pblk[FP];
+    // scale rows of the P fragments: gate/up, one for the gate rows and one for
+    // each fragment of up rows; else one for each half of the tile
+    int pblk[NSP];
 #pragma unroll
-    for (int i = 0; i < FP; ++i) pblk[i] = p_block<GU, BP>(g, p0, prow[i] + lr);
+    for (int i = 0; i < NSP; ++i) pblk[i] = GU && i > 0 ? p_block<GU, BP>(g, p0, prow[i + 1] + lr) : i;
     // every wave's loads of stage 0 and the scales have landed (it waited for
     // them), and every wave is done with the epilogue's slots
     wait_lgkm();
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
+    // (what a spill brings back has to be here before the loop: a wait for it
+    // among the stages would wait for all loads)
+    ld.keep();
+    uint32_t at_keep = at0;
+    asm volatile("" : "+v"(at_keep));
     if (more && gathered) load_slots(tn);
     ld.issue(128, L::STAGE);
 
@@ -677,11 +723,11 @@ __global__ __launch_bounds__(512, 2) void k_grouped_fp8_wide(Fp8Args g) {
       qf[j][s] = frag(lds + (qrow0 + 128 * j) * 128, at ^ (s ? 64u : 0u), 32u);
     };
     // scales: of the stage at hand in the lowest byte, of the next ones above it
-    uint32_t sp[FP], sq[FQ], sp4[FP], sq4[FQ];
+    uint32_t sp[NSP], sq[FQ], sp4[NSP], sq4[FQ];
     auto scales = [&](int n) {
       const int w = ((unsigned)n % kScaleChunk) >> 2;
 #pragma unroll
-      for (int i = 0; i < FP; ++i) sp4[i] = s_ps[w][pblk[i]];
+      for (int i = 0; i < NSP; ++i) sp4[i] = s_ps[w][pblk[i]];
 #pragma unroll
       for (int j = 0; j < FQ; ++j) sq4[j] = s_qs[w][qrow0 + 128 * j + lr];
     };
@@ -694,18 +740,18 @@ __global__ __launch_bounds__(512, 2) void k_grouped_fp8_wide(Fp8Args g) {
     }
     scales(0);
 #pragma unroll
-    for (int i = 0; i < FP; ++i) sp[i] = sp4[i];
+    for (int i = 0; i < NSP; ++i) sp[i] = sp4[i];
 #pragma unroll
     for (int j = 0; j < FQ; ++j) sq[j] = sq4[j];
     // NL: the wave's Q fragments that hold rows
     auto run = [&](auto nl) {
       constexpr int NL = decltype(nl)::value;
-      uint32_t at = at0, k0 = 256;   // stage n's place; byte of stage n + 2
+      uint32_t at = at_keep, k0 = 256;   // stage n's place; byte of stage n + 2
       auto mfma = [&](int h, int i, int s) {
 #pragma unroll
         for (int j = 0; j < NL; ++j)
           acc[2 * h + i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-              pf[i][s], qf[j][s], acc[2 * h + i][j], 0, 0, 0, (int)sp[2 * h + i], 0, (int)sq[j]);
+              pf[i][s], qf[j][s], acc[2 * h + i][j], 0, 0, 0, (int)sp[GU ? (h ? i + 1 : 0) : h], 0, (int)sq[j]);
       };
       // What the next half reads has landed everywhere (8 younger loads are on
       // their way), and what this half was read from is free.
@@ -765,7 +811,7 @@ __global__ __launch_bounds__(512, 2) void k_grouped_fp8_wide(Fp8Args g) {
           k0 += 128;
           const bool fresh = ((n + 1) & 3) == 0;
 #pragma unroll
-          for (int i = 0; i < FP; ++i) sp[i] = fresh ? sp4[i] : sp[i] >> 8;
+          for (int i = 0; i < NSP; ++i) sp[i] = fresh ? sp4[i] : sp[i] >> 8;
 #pragma unroll
           for (int j = 0; j < FQ; ++j) sq[j] = fresh ? sq4[j] : sq[j] >> 8;
         }
@@ -778,7 +824,7 @@ __global__ __launch_bounds__(512, 2) void k_grouped_fp8_wide(Fp8Args g) {
         asm volatile("" ::: "memory");
         scales(n);
 #pragma unroll
-        for (int i = 0; i < FP; ++i) sp[i] = sp4[i];
+        for (int i = 0; i < NSP; ++i) sp[i] = sp4[i];
 #pragma unroll
         for (int j = 0; j < FQ; ++j) sq[j] = sq4[j];
       }
@@ -898,7 +944,6 @@ __global__ __launch_bounds__(512, 2) void k_grouped_fp8_wide(Fp8Args g) {
     if (nlive == 0) wait_vm<0>();
     if (!more) break;
     t = tn;
-    id = next;
   }
 }
 
@@ -924,20 +969,21 @@ __global__ __launch_bounds__(NW * 64) void k_grouped_fp8_small(Fp8Args g) {
   __shared__ uint32_t s_qs[kScaleChunk / 4][BQ];
   __shared__ uint32_t s_ps[kScaleChunk / 4][4];
   __shared__ float s_amax[GU ? NW : 1][GU ? BQ : 1];
-  static_assert(sizeof(Tiles) <= sizeof(smem), "the tables share the ring");
-  Tiles &tiles = *reinterpret_cast<Tiles *>(smem);
+  using Table = Tiles<BQ, 1>;
+  static_assert(sizeof(Table) <= sizeof(smem), "the table shares the ring");
+  Table &tiles = *reinterpret_cast<Table *>(smem);
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int N = g.N, nk = scale_blocks(g.K), cols = scale_cols(g.K);
   const bool gathered = g.row_to_slot != nullptr;
 
-  tiles.template init<BQ>(g);
-  const int total = tiles.total(g), chunk = (total + 7) >> 3;
+  tiles.init(g);
+  const int total = tiles.total(g, 0), chunk = (total + 7) >> 3;
   const int id = (int)(blockIdx.x & 7) * chunk + (int)(blockIdx.x >> 3);
   if ((int)(blockIdx.x >> 3) >= chunk || id >= total) return;
-  const Tile t = tiles.template decode<BQ>(g, id);
-  __syncthreads();   // the tables give way to the ring
+  const Tile t = tiles.decode(g, 0, id);
+  __syncthreads();   // the table gives way to the ring
   const int p0 = t.pt * (GU ? BP / 2 : BP);
   const int lr = lane & 15, lg = lane >> 4;
   int prow[FP], pblk[FP];
