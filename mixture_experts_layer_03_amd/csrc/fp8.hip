@@ -123,9 +123,12 @@ __global__ __launch_bounds__(256) void k_quant_rows(const T *__restrict__ x, int
 // ------------------------------------------------------------------ weights
 //
 // One block of threads per 128 x 128 weight block: thread t holds columns
-// 8 (t % 16).. of rows t / 16 + 16 i.  The transposed copy goes through LDS,
-// and its scale is the same byte: a square block keeps its scale when it is
-// transposed.
+// 8 (t % 16).. of rows 4 (t / 16) .. + 3 and 64 further.  The transposed copy
+// goes through LDS, four rows of a column to a dword, chunk c of 16 bytes of
+// the transposed row r at place c ^ (r / 8 % 8); its scale is the same byte: a
+// square block keeps its scale when it is transposed.  32 x 5760 x 2880 bf16
+// into both layouts: 415 us (5.1 TB/s read and written; 521 with byte writes to
+// LDS).
 template <typename T, bool TR>
 __global__ __launch_bounds__(256) void k_quant_weights(const T *__restrict__ w, int N, int K,
                                                        uint8_t *__restrict__ q,
@@ -133,7 +136,7 @@ __global__ __launch_bounds__(256) void k_quant_weights(const T *__restrict__ w, 
                                                        uint8_t *__restrict__ qt,
                                                        uint8_t *__restrict__ scale_t) {
   __shared__ float s_max[4];
-  __shared__ __attribute__((aligned(16))) uint8_t s_t[TR ? 128 * 144 : 16];
+  __shared__ __attribute__((aligned(16))) uint8_t s_t[TR ? 128 * 128 : 16];
   const int tid = threadIdx.x, cg = tid & 15, rg = tid >> 4;
   const int kb = blockIdx.x, mb = blockIdx.y;
   const int64_t e = blockIdx.z;
@@ -143,7 +146,7 @@ __global__ __launch_bounds__(256) void k_quant_weights(const T *__restrict__ w, 
   float m = 0.0f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int n = mb * kBlk + rg + 16 * i;
+    const int n = mb * kBlk + 4 * rg + i % 4 + 16 * (i & 4);
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
     if (n < N && c < K) load8(we + (int64_t)n * K + c, v[i]);
@@ -167,21 +170,33 @@ __global__ __launch_bounds__(256) void k_quant_weights(const T *__restrict__ w, 
     if (mb == mbs - 1 && tid > 64 && tid - 64 < cols_t - mb)
       scale_t[(e * nbs + kb) * cols_t + mb + tid - 64] = 127;
   }
+  uint32_t lo[8], hi[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int n = mb * kBlk + rg + 16 * i;
+    const int n = mb * kBlk + 4 * rg + i % 4 + 16 * (i & 4);
     float u[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) u[j] = scaled(v[i][j], inv);
-    const uint32_t lo = pack_e4m3x4(u[0], u[1], u[2], u[3]);
-    const uint32_t hi = pack_e4m3x4(u[4], u[5], u[6], u[7]);
-    if (n < N && c < K) *reinterpret_cast<u32x2_t *>(q + (e * N + n) * K + c) = u32x2_t{lo, hi};
-    if (TR) {
-      const int rl = rg + 16 * i;
+    lo[i] = pack_e4m3x4(u[0], u[1], u[2], u[3]);
+    hi[i] = pack_e4m3x4(u[4], u[5], u[6], u[7]);
+    if (n < N && c < K) *reinterpret_cast<u32x2_t *>(q + (e * N + n) * K + c) = u32x2_t{lo[i], hi[i]};
+  }
+  if (TR) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        s_t[(cg * 8 + j) * 144 + rl] = (uint8_t)(lo >> (8 * j));
-        s_t[(cg * 8 + 4 + j) * 144 + rl] = (uint8_t)(hi >> (8 * j));
+    for (int h = 0; h < 2; ++h) {      // rows 4 rg .. of the upper and the lower half
+      const int chunk = (4 * h + (rg >> 2)) ^ (cg & 7);
+      uint8_t *const to = s_t + cg * 8 * 128 + chunk * 16 + (rg & 3) * 4;
+#pragma unroll
+      for (int d = 0; d < 2; ++d) {    // columns 8 cg + 4 d ..
+        const uint32_t *const w4 = (d ? hi : lo) + 4 * h;
+        const uint32_t a = __builtin_amdgcn_perm(w4[1], w4[0], 0x05010400u);   // columns 0, 1 of rows 0, 1
+        const uint32_t b = __builtin_amdgcn_perm(w4[1], w4[0], 0x07030602u);   // columns 2, 3
+        const uint32_t f = __builtin_amdgcn_perm(w4[3], w4[2], 0x05010400u);
+        const uint32_t g = __builtin_amdgcn_perm(w4[3], w4[2], 0x07030602u);
+        *reinterpret_cast<uint32_t *>(to + (4 * d + 0) * 128) = __builtin_amdgcn_perm(f, a, 0x05040100u);
+        *reinterpret_cast<uint32_t *>(to + (4 * d + 1) * 128) = __builtin_amdgcn_perm(f, a, 0x07060302u);
+        *reinterpret_cast<uint32_t *>(to + (4 * d + 2) * 128) = __builtin_amdgcn_perm(g, b, 0x05040100u);
+        *reinterpret_cast<uint32_t *>(to + (4 * d + 3) * 128) = __builtin_amdgcn_perm(g, b, 0x07060302u);
       }
     }
   }
@@ -193,7 +208,7 @@ __global__ __launch_bounds__(256) void k_quant_weights(const T *__restrict__ w, 
       const int kr = (tid >> 3) + 32 * i, n = mb * kBlk + (tid & 7) * 16;
       if (kb * kBlk + kr < K && n < N)
         *reinterpret_cast<u32x4_t *>(qt + (e * K + kb * kBlk + kr) * N + n) =
-            *reinterpret_cast<const u32x4_t *>(s_t + kr * 144 + (tid & 7) * 16);
+            *reinterpret_cast<const u32x4_t *>(s_t + kr * 128 + (((tid & 7) ^ (kr >> 3)) & 7) * 16);
     }
   }
 }
