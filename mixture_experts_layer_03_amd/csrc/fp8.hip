@@ -849,10 +849,25 @@ __global__ __launch_bounds__(512, 2) void k_grouped_fp8_wide(Fp8Args g) {
     else if (nlive == 1) run(std::integral_constant<int, 1>{});
     else run(std::integral_constant<int, 0>{});
 
+    // Epilogue.  The lane number is taken anew: addresses kept over the main
+    // loop would not fit its registers.
+    int ln = lane;
+    asm volatile("" : "+v"(ln));
+    const int er = ln & 31, eg = ln >> 5;
+    const int64_t r0 = (int64_t)t.seg0 + t.q0;
+    float w[FQ];   // row weights, asked for before the next tile's loads
+    if (!GU) {
+#pragma unroll
+      for (int j = 0; j < FQ; ++j) {
+        const int q = qrow0 + 128 * j + er;
+        w[j] = g.row_scale && q < t.qvalid ? g.row_scale[r0 + q] : 1.0f;
+      }
+    }
     // every wave is done with the ring (the empty stages' zeros too) and the scales
     asm volatile("" ::: "memory");
     wait_vm<0>();
     __builtin_amdgcn_s_barrier();
+    if (!GU) asm volatile("" : "+v"(w[0]), "+v"(w[1]) : : "memory");
     asm volatile("" ::: "memory");
     if (more) {
       set_tile(tn);
@@ -860,15 +875,9 @@ __global__ __launch_bounds__(512, 2) void k_grouped_fp8_wide(Fp8Args g) {
       load_scales(tn, 0);
     }
 
-    // Epilogue.  Lane holds D[8 (v / 4) + 4 (lane / 32) + v % 4][lane % 32] of each fragment;
+    // Lane holds D[8 (v / 4) + 4 (lane / 32) + v % 4][lane % 32] of each fragment;
     // the results go through the wave's own slot in the ring's second place,
     // so that the stores are 16 bytes per lane.
-    // (The lane number is taken anew: addresses kept over the main loop would
-    // not fit its registers.)
-    int ln = lane;
-    asm volatile("" : "+v"(ln));
-    const int er = ln & 31, eg = ln >> 5;
-    const int64_t r0 = (int64_t)t.seg0 + t.q0;
     LDS_AS char *const slot = (LDS_AS char *)smem + L::STAGE + wave * (L::STAGE / NW);
     if constexpr (GU) {
       constexpr int PITCH = 64 + 16;
@@ -936,15 +945,13 @@ __global__ __launch_bounds__(512, 2) void k_grouped_fp8_wide(Fp8Args g) {
 #pragma unroll
       for (int j = 0; j < FQ; ++j) {
         if (j >= nlive) continue;
-        const int q = qrow0 + 128 * j + er;
-        const float w = g.row_scale && q < t.qvalid ? g.row_scale[r0 + q] : 1.0f;
 #pragma unroll
         for (int i = 0; i < FP; ++i)
 #pragma unroll
           for (int v = 0; v < 16; v += 4)
             *reinterpret_cast<LDS_AS u32x2_t *>(slot + er * 256 + ((4 * i + v / 4) ^ (er & 15)) * 16 + 8 * eg) =
-                u32x2_t{pack_bf16x2(w * acc[i][j][v], w * acc[i][j][v + 1]),
-                        pack_bf16x2(w * acc[i][j][v + 2], w * acc[i][j][v + 3])};
+                u32x2_t{pack_bf16x2(w[j] * acc[i][j][v], w[j] * acc[i][j][v + 1]),
+                        pack_bf16x2(w[j] * acc[i][j][v + 2], w[j] * acc[i][j][v + 3])};
         if (j == 0) wait_vm<0>();   // the next tile's loads; before the stores, which need not be waited for
 #pragma unroll
         for (int rr = 0; rr < 32; rr += 4) {   // 16 lanes x 16 bytes per row
@@ -952,7 +959,9 @@ __global__ __launch_bounds__(512, 2) void k_grouped_fp8_wide(Fp8Args g) {
           const u32x4_t val =
               *reinterpret_cast<const LDS_AS u32x4_t *>(slot + row * 256 + (ch ^ (row & 15)) * 16);
           const int qq = qrow0 + 128 * j + row, n = p0 + wp * 64 + (ch >> 3) * 128 + (ch & 7) * 8;
-          if (qq < t.qvalid && n < N) *reinterpret_cast<u32x4_t *>(g.c + (r0 + qq) * N + n) = val;
+          // (written once, read by another kernel: kept out of the way of the weights in L2)
+          if (qq < t.qvalid && n < N)
+            __builtin_nontemporal_store(val, reinterpret_cast<u32x4_t *>(g.c + (r0 + qq) * N + n));
         }
       }
     }
