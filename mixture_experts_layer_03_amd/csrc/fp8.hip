@@ -127,8 +127,8 @@ __global__ __launch_bounds__(256) void k_quant_rows(const T *__restrict__ x, int
 // goes through LDS, four rows of a column to a dword, chunk c of 16 bytes of
 // the transposed row r at place c ^ (r / 8 % 8); its scale is the same byte: a
 // square block keeps its scale when it is transposed.  32 x 5760 x 2880 bf16
-// into both layouts: 415 us (5.1 TB/s read and written; 521 with byte writes to
-// LDS).
+// into both layouts: 393 us (5.4 TB/s read and written; 411 with stores that
+// stay in L2, 521 with those and byte writes to LDS).
 template <typename T, bool TR>
 __global__ __launch_bounds__(256) void k_quant_weights(const T *__restrict__ w, int N, int K,
                                                        uint8_t *__restrict__ q,
@@ -179,7 +179,8 @@ __global__ __launch_bounds__(256) void k_quant_weights(const T *__restrict__ w, 
     for (int j = 0; j < 8; ++j) u[j] = scaled(v[i][j], inv);
     lo[i] = pack_e4m3x4(u[0], u[1], u[2], u[3]);
     hi[i] = pack_e4m3x4(u[4], u[5], u[6], u[7]);
-    if (n < N && c < K) *reinterpret_cast<u32x2_t *>(q + (e * N + n) * K + c) = u32x2_t{lo[i], hi[i]};
+    if (n < N && c < K)
+      __builtin_nontemporal_store(u32x2_t{lo[i], hi[i]}, reinterpret_cast<u32x2_t *>(q + (e * N + n) * K + c));
   }
   if (TR) {
 #pragma unroll
@@ -207,8 +208,9 @@ __global__ __launch_bounds__(256) void k_quant_weights(const T *__restrict__ w, 
     for (int i = 0; i < 4; ++i) {
       const int kr = (tid >> 3) + 32 * i, n = mb * kBlk + (tid & 7) * 16;
       if (kb * kBlk + kr < K && n < N)
-        *reinterpret_cast<u32x4_t *>(qt + (e * K + kb * kBlk + kr) * N + n) =
-            *reinterpret_cast<const u32x4_t *>(s_t + kr * 128 + (((tid & 7) ^ (kr >> 3)) & 7) * 16);
+        __builtin_nontemporal_store(
+            *reinterpret_cast<const u32x4_t *>(s_t + kr * 128 + (((tid & 7) ^ (kr >> 3)) & 7) * 16),
+            reinterpret_cast<u32x4_t *>(qt + (e * K + kb * kBlk + kr) * N + n));
     }
   }
 }
@@ -268,7 +270,14 @@ __device__ __forceinline__ void dma16(u32x4_t rs, uint32_t lds, uint32_t voff) {
                : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(voff), "s"(rs)
                : "memory", "m0");
 }
-// The same with 4 bytes per lane (lane l at lds + 4 l).
+// The same for what is read once: its lines do not stay in L2.
+__device__ __forceinline__ void dma16_once(u32x4_t rs, uint32_t lds, uint32_t voff) {
+  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen nt lds"
+               :
+               : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(voff), "s"(rs)
+               : "memory", "m0");
+}
+// The same as dma16 with 4 bytes per lane (lane l at lds + 4 l).
 __device__ __forceinline__ void dma4(u32x4_t rs, uint32_t lds, uint32_t voff) {
   asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, 0 offen lds"
                :
@@ -378,7 +387,12 @@ struct Tiles {
 // experts: 28.9 -> 25.1 us at one token, 108 -> 104 at 64, 115 -> 109 at 256);
 // in the product into d its start costs as much as it saves (13.8 -> 15.4,
 // 59.5 -> 59.0).
-template <bool GU, int BP, int BQ, int NW, bool LATE>
+//
+// ONCE: the weight rows are read by one tile only and need not stay in L2 (d =
+// f = 2880, 32 experts, gate/up + down: 16 tokens 98 + 54 -> 89 + 54 us, 64
+// 104 + 59 -> 94 + 58, 256 109 + 70 -> 101 + 71; where several tiles of rows
+// share them, 5003 rows of 13 experts, 720 x 1136, it costs: 13 -> 18).
+template <bool GU, int BP, int BQ, int NW, bool LATE, bool ONCE>
 struct Loads {
   static constexpr int TP = BP * 8, TQ = BQ * 8;               // 16-byte chunks of a stage
   static constexpr int NIP = TP / 64 / NW;                     // instructions per wave and stage
@@ -447,13 +461,17 @@ struct Loads {
   // one(i): instruction i of the stage at byte k0 of the rows, into the place
   // of the ring at `buf`
   __device__ __forceinline__ void one(int i, uint32_t k0, uint32_t buf) const {
-    const bool isp = i < NIP;
-    const int j = isp ? i : i - NIP;
-    const uint32_t bytes = isp ? pbytes : qbytes;
-    const u32x4_t rs = make_rsrc((isp ? pbase : qbase) + k0, max(bytes, k0) - k0);
-    const uint32_t to = (isp ? ldsP : ldsQ) + buf + (uint32_t)j * 1024u;
-    dma16(rs, SPARE && !isp && wave * 8 >= BQ ? spare : to,
-          k0 < (isp ? leftP[j & 1] : leftQ[NIQ == 1 ? 0 : j & 1]) ? (isp ? voffP[isp ? j : 0] : voffQ[isp ? 0 : j]) : kOOB);
+    if (i < NIP) {
+      const u32x4_t rs = make_rsrc(pbase + k0, max(pbytes, k0) - k0);
+      const uint32_t to = ldsP + buf + (uint32_t)i * 1024u, voff = k0 < leftP[i & 1] ? voffP[i] : kOOB;
+      if (ONCE) dma16_once(rs, to, voff);
+      else dma16(rs, to, voff);
+    } else {
+      const int j = i - NIP;
+      dma16(make_rsrc(qbase + k0, max(qbytes, k0) - k0),
+            SPARE && wave * 8 >= BQ ? spare : ldsQ + buf + (uint32_t)j * 1024u,
+            k0 < leftQ[NIQ == 1 ? 0 : j & 1] ? voffQ[j] : kOOB);
+    }
   }
   // stage -1: the first 64 bytes of the late rows, as the stage's second half
   __device__ __forceinline__ void pre(const Fp8Args &g, uint32_t buf) const {
@@ -971,7 +989,8 @@ __global__ __launch_bounds__(512, 2) void k_grouped_fp8_wide(Fp8Args g) {
   }
 }
 
-// Few rows per expert, where the weights' way from memory bounds, and few
+// Few rows per expert, where the weights' way from memory bounds (64 tokens, 4
+// of 32 experts, d = f = 2880: 531 MB of gate/up weights in 92 us), and few
 // tiles, where one tile's latency does: tiles of BP weight rows (gate/up: 128
 // gate and 128 up, one block of h) and 64 rows, a block of threads each, over
 // all of K with NS - 1 stages on their way.  NW waves side by side along the
@@ -983,10 +1002,10 @@ __global__ __launch_bounds__(512, 2) void k_grouped_fp8_wide(Fp8Args g) {
 // product: 28 against 30 us at 4 tokens, 49 against 53 at 16, 57 against 58 at
 // 64 (265 MB: 4.7 TB/s).  More rows want more work per byte loaded: 1024 rows,
 // 8 experts, 608 x 608: 9.1 and 9.4 us; 4096 rows: 15.7 and 11.8 us.
-template <bool GU, int BP, int NS, int NW, bool LATE>
+template <bool GU, int BP, int NS, int NW, bool LATE, bool ONCE>
 __global__ __launch_bounds__(NW * 64) void k_grouped_fp8_small(Fp8Args g) {
   constexpr int BQ = 64, FP = BP / NW / 16, FQ = BQ / 16;
-  using L = Loads<GU, BP, BQ, NW, LATE>;
+  using L = Loads<GU, BP, BQ, NW, LATE, ONCE>;
   static_assert(!GU || BP == 256, "a gate/up tile holds one block of 128 h");
   static_assert((NS - 2) * L::LOADS < 64, "vmcnt range");
   __shared__ u32x4_t smem[NS * (L::TP + L::TQ) + 64];
@@ -1171,12 +1190,14 @@ __global__ __launch_bounds__(NW * 64) void k_grouped_fp8_small(Fp8Args g) {
 
 // Rows per expert (on average, of those that can have rows) up to which the
 // weights bound.  d = f = 2880, 32 experts, gate/up + down, small tiles (BP =
-// 64) against the wide kernel: 104 + 57 us against 107 + 67 at 8 rows, 110 + 67
-// against 111 + 69 at 32, 116 + 74 against 115 + 71 at 48.
-constexpr int64_t kFewRows = 32;
+// 64) against the wide kernel: 91 + 56 us against 107 + 66 at 8 rows, 97 + 67
+// against 110 + 69 at 32, 103 + 77 against 115 + 70 at 48, 124 + 87 against
+// 115 + 71 at 56.
+template <bool GU>
+constexpr int64_t kFewRows = GU ? 48 : 32;
 constexpr int kCUs = 256;   // persistent kernels: one block of threads per CU, a multiple of 8
 
-template <bool GU, int BP, int NS, int NW, bool LATE>
+template <bool GU, int BP, int NS, int NW, bool LATE, bool ONCE>
 int launch_small(Fp8Args g, int64_t active, const char *name, const char *fn, hipStream_t s) {
   constexpr int per = GU ? BP / 2 : BP;
   g.PT = (g.N + per - 1) / per;
@@ -1184,7 +1205,7 @@ int launch_small(Fp8Args g, int64_t active, const char *name, const char *fn, hi
   const int64_t tiles = (g.slots / 64 + active) * g.PT;
   MOE_REQUIRE(tiles < ((int64_t)1 << 30), MOE_ERR_UNSUPPORTED, "%s: too many tiles", fn);
   const unsigned blocks = (unsigned)((tiles + 7) / 8 * 8);
-  MOE_LAUNCH(name, s, (k_grouped_fp8_small<GU, BP, NS, NW, LATE><<<blocks, NW * 64, 0, s>>>(g)));
+  MOE_LAUNCH(name, s, (k_grouped_fp8_small<GU, BP, NS, NW, LATE, ONCE><<<blocks, NW * 64, 0, s>>>(g)));
   return check_launch(fn);
 }
 
@@ -1192,10 +1213,10 @@ template <bool GU>
 int product(const Fp8Args &args, const char *name, const char *fn, hipStream_t s) {
   Fp8Args g = args;
   const int64_t active = g.E < g.slots ? (int64_t)g.E : g.slots;   // experts with rows, at most
-  if (g.slots <= kFewRows * active) {
+  if (g.slots <= kFewRows<GU> * active) {
     if constexpr (GU)
-      if (g.K % 128 == 64) return launch_small<GU, 256, 3, 8, true>(g, active, name, fn, s);
-    return launch_small<GU, GU ? 256 : 64, GU ? 3 : 4, GU ? 8 : 4, false>(g, active, name, fn, s);
+      if (g.K % 128 == 64) return launch_small<GU, 256, 3, 8, true, true>(g, active, name, fn, s);
+    return launch_small<GU, GU ? 256 : 64, GU ? 3 : 4, GU ? 8 : 4, false, true>(g, active, name, fn, s);
   }
   // Many rows, but so few small tiles (counting half a tile of 64 rows lost per
   // expert) that all run at once: gate/up one, else two blocks of threads to a
@@ -1205,7 +1226,8 @@ int product(const Fp8Args &args, const char *name, const char *fn, hipStream_t s
   // against 17.9; 1024 rows, 4 experts, 2880 x 2880 (414) 51 against 42 and 27
   // against 37; 2048 rows (782) 44 against 39.
   const int64_t small = (g.slots / 64 + active / 2) * ((g.N + 127) / 128);
-  if (small <= (GU ? kCUs : 2 * kCUs)) return launch_small<GU, GU ? 256 : 128, 3, 8, false>(g, active, name, fn, s);
+  if (small <= (GU ? kCUs : 2 * kCUs))
+    return launch_small<GU, GU ? 256 : 128, 3, 8, false, false>(g, active, name, fn, s);
   const int per = GU ? 128 : 256;
   g.PT = (g.N + per - 1) / per;
   const int64_t tiles = (g.slots / 256 + active) * g.PT;
