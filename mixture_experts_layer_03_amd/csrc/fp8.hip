@@ -16,7 +16,12 @@
 // first, cut at 2^-13 of the largest one's power of two (measured), then the
 // groups' sums and the accumulator in fp32.  The cut is taken for its rate
 // (twice that of bf16): the values have 4 significant bits, and the error it
-// leaves, about 1e-4 of a result, is a tenth of the bf16 store's.
+// leaves, about 1e-4 of a result, is a tenth of the bf16 store's.  The gate/up
+// product of few rows does without it: h is rounded to 8 bits at once, and
+// where the cut moves a value over a border h changes by a step of 6 to 12%.
+// In many values that adds a little to the rounding's own error (0.0020
+// against 0.0017 of y); one token's few values can meet one such step too many
+// (0.0038), so there the bytes become bf16, whose products are exact.
 #include <type_traits>
 
 #include "moe_internal.h"
@@ -384,14 +389,14 @@ struct Tiles {
 // this stage's first.  Stages that straddle lines ask for every such line
 // twice: 92 blocks of threads reading 256 rows of 2880 bytes take 19.5 us, of
 // 2944 bytes 14.8.  The gate/up product of few rows has it (d = f = 2880, 32
-// experts: 28.9 -> 25.1 us at one token, 108 -> 104 at 64, 115 -> 109 at 256);
-// in the product into d its start costs as much as it saves (13.8 -> 15.4,
-// 59.5 -> 59.0).
+// experts: 28.9 -> 25.1 us at one token, 108 -> 104 at 64, 115 -> 109 at 256,
+// before ONCE); in the product into d its start costs as much as it saves
+// (13.8 -> 15.4, 59.5 -> 59.0).
 //
 // ONCE: the weight rows are read by one tile only and need not stay in L2 (d =
-// f = 2880, 32 experts, gate/up + down: 16 tokens 98 + 54 -> 89 + 54 us, 64
-// 104 + 59 -> 94 + 58, 256 109 + 70 -> 101 + 71; where several tiles of rows
-// share them, 5003 rows of 13 experts, 720 x 1136, it costs: 13 -> 18).
+// f = 2880, 32 experts, gate/up + down, before bf16: 16 tokens 98 + 54 -> 89 +
+// 54 us, 64 104 + 59 -> 94 + 58, 256 109 + 70 -> 101 + 71; where several tiles
+// of rows share them, 5003 rows of 13 experts, 720 x 1136, it costs: 13 -> 18).
 template <bool GU, int BP, int BQ, int NW, bool LATE, bool ONCE>
 struct Loads {
   static constexpr int TP = BP * 8, TQ = BQ * 8;               // 16-byte chunks of a stage
@@ -493,6 +498,18 @@ template <bool GU, int BP>
 __device__ __forceinline__ int p_block(const Fp8Args &g, int p0, int r) {
   if (!GU) return r / kBlk;
   return r < BP / 2 ? 0 : 1 + (g.N + p0 + r - BP / 2) / kBlk - (g.N + p0) / kBlk;
+}
+
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+
+// Values 8 m .. of a fragment's 32 as bf16 (exact: 4 significant bits), unscaled.
+__device__ __forceinline__ bf16x8_t as_bf16(const i32x8_t &f, int m) {
+  typedef __bf16 pair_t __attribute__((ext_vector_type(2)));
+  const pair_t a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)f[2 * m], 1.0f, false);
+  const pair_t b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)f[2 * m], 1.0f, true);
+  const pair_t c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)f[2 * m + 1], 1.0f, false);
+  const pair_t d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)f[2 * m + 1], 1.0f, true);
+  return bf16x8_t{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
 // 32 bytes of a fragment: chunks at `at` and at `at` with the bits `other` flipped.
@@ -990,12 +1007,14 @@ __global__ __launch_bounds__(512, 2) void k_grouped_fp8_wide(Fp8Args g) {
 }
 
 // Few rows per expert, where the weights' way from memory bounds (64 tokens, 4
-// of 32 experts, d = f = 2880: 531 MB of gate/up weights in 92 us), and few
+// of 32 experts, d = f = 2880: 531 MB of gate/up weights in 96 us), and few
 // tiles, where one tile's latency does: tiles of BP weight rows (gate/up: 128
 // gate and 128 up, one block of h) and 64 rows, a block of threads each, over
 // all of K with NS - 1 stages on their way.  NW waves side by side along the
 // weight rows, 16 x 16 fragments (MFMA 16x16x128, one per stage and fragment
-// pair; fragments past the expert's last row are left out).
+// pair; fragments past the expert's last row are left out).  The gate/up
+// product of few rows converts its fragments to bf16 (the rounding of h, at the
+// top); that costs 24.8 -> 28.3 us at one token, 92 -> 96 at 64.
 //
 // One CU draws about 50 GB/s from memory however much it has on its way, so
 // few rows want many tiles: d = f = 2880, 32 experts, BP = 64 against 128, down
@@ -1007,6 +1026,7 @@ __global__ __launch_bounds__(NW * 64) void k_grouped_fp8_small(Fp8Args g) {
   constexpr int BQ = 64, FP = BP / NW / 16, FQ = BQ / 16;
   using L = Loads<GU, BP, BQ, NW, LATE, ONCE>;
   static_assert(!GU || BP == 256, "a gate/up tile holds one block of 128 h");
+  constexpr bool EXACT = GU && ONCE;   // bf16 products, scales applied to their sums over a stage
   static_assert((NS - 2) * L::LOADS < 64, "vmcnt range");
   __shared__ u32x4_t smem[NS * (L::TP + L::TQ) + 64];
   __shared__ uint32_t s_qs[kScaleChunk / 4][BQ];
@@ -1111,15 +1131,39 @@ __global__ __launch_bounds__(NW * 64) void k_grouped_fp8_small(Fp8Args g) {
       pf[i] = i32x8_t{(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
       sp[i] = s_ps[w][pblk[i]] >> sh;
     }
+    bf16x8_t pb[EXACT ? FP : 1][4];
+    if constexpr (EXACT)
+#pragma unroll
+      for (int i = 0; i < FP; ++i)
+#pragma unroll
+        for (int m = 0; m < 4; ++m) pb[i][m] = as_bf16(pf[i], m);
 #pragma unroll
     for (int j = 0; j < FQ; ++j) {
       if (j < nlive) {
         const i32x8_t qf = frag(lds + L::TP * 16 + 16 * j * 128, buf + at0, 64u);
         const uint32_t sq = s_qs[w][16 * j + lr] >> sh;
+        if constexpr (EXACT) {
+          f32x4_t part[FP];
 #pragma unroll
-        for (int i = 0; i < FP; ++i)
-          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-              pf[i], qf, acc[i][j], 0, 0, 0, (int)sp[i], 0, (int)sq);
+          for (int i = 0; i < FP; ++i) part[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            const bf16x8_t qb = as_bf16(qf, m);
+#pragma unroll
+            for (int i = 0; i < FP; ++i)
+              part[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(pb[i][m], qb, part[i], 0, 0, 0);
+          }
+#pragma unroll
+          for (int i = 0; i < FP; ++i)
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+              acc[i][j][v] += ldexpf(part[i][v], (int)(sp[i] & 255u) + (int)(sq & 255u) - 254);
+        } else {
+#pragma unroll
+          for (int i = 0; i < FP; ++i)
+            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                pf[i], qf, acc[i][j], 0, 0, 0, (int)sp[i], 0, (int)sq);
+        }
       }
     }
     buf = buf == (NS - 1) * L::STAGE ? 0u : buf + L::STAGE;
@@ -1190,11 +1234,11 @@ __global__ __launch_bounds__(NW * 64) void k_grouped_fp8_small(Fp8Args g) {
 
 // Rows per expert (on average, of those that can have rows) up to which the
 // weights bound.  d = f = 2880, 32 experts, gate/up + down, small tiles (BP =
-// 64) against the wide kernel: 91 + 56 us against 107 + 66 at 8 rows, 97 + 67
-// against 110 + 69 at 32, 103 + 77 against 115 + 70 at 48, 124 + 87 against
-// 115 + 71 at 56.
+// 64) against the wide kernel: 95 + 56 us against 107 + 66 at 8 rows, 102 + 60
+// against 108 + 67 at 16, 112 + 64 against 110 + 68 at 24, 116 + 67 against
+// 110 + 69 at 32, 120 + 72 against 112 + 69 at 40.
 template <bool GU>
-constexpr int64_t kFewRows = GU ? 48 : 32;
+constexpr int64_t kFewRows = GU ? 20 : 32;
 constexpr int kCUs = 256;   // persistent kernels: one block of threads per CU, a multiple of 8
 
 template <bool GU, int BP, int NS, int NW, bool LATE, bool ONCE>

@@ -261,3 +261,35 @@ def test_quantisation_past_2_31_elements():
     torch.cuda.synchronize()
     for p, q in zip(out, last):
         assert torch.equal(p[-1:], q)
+
+
+@pytest.mark.parametrize("counts,d,f", [([1, 0, 3], 2880, 1040), ([2, 9, 1, 17], 512, 720), ([19], 720, 1296)],
+                         ids=["d2880", "d512", "d720"])
+def test_gate_up_of_few_rows_cuts_no_products(counts, d, f):
+    """448 * 448 - 448 * 448 + u within 8 consecutive k is u, and silu(32) u = 32 u (e^-32 is below half a unit):
+    whole numbers that h holds exactly."""
+    import torch
+    from mixture_experts_layer_03_amd import abi
+    dev = need_gpu()
+    print("GPU case few rows", counts, d, f, flush=True)
+    E, R = len(counts), sum(counts)
+    x, w = np.zeros((R, d)), np.zeros((E, 2 * f, d))
+    x[:, 0::8], x[:, 1::8], x[:, 2::8] = 448, 448, 1
+    j = np.arange(f)
+    u = np.empty((E, f))
+    for e in range(E):
+        k = 8 * ((j + 5 * e) % (d // 8))
+        u[e] = (j + e) % 7 + 1
+        w[e, j, k + 2] = 32
+        w[e, f + j, k], w[e, f + j, k + 1], w[e, f + j, k + 2] = 448, -448, u[e]
+    one = dict(fill_value=127, dtype=torch.uint8, device=dev)
+    u8 = dict(dtype=torch.uint8, device=dev)
+    h, hs = torch.empty(R, f, **u8), torch.empty(R, S.scale_cols(f), **u8)
+    y = torch.empty(R, d, dtype=torch.bfloat16, device=dev)
+    abi.moe_grouped_ffn_fwd_fp8(_u8(S.to_e4m3(x), dev), torch.full((R, S.scale_cols(d)), **one), _i32(_offsets(counts), dev),
+                                _u8(S.to_e4m3(w), dev), torch.full((E, -(-2 * f // 128), S.scale_cols(d)), **one),
+                                torch.zeros(E, d, f, **u8), torch.full((E, -(-d // 128), S.scale_cols(f)), **one), None, h,
+                                hs, y)
+    torch.cuda.synchronize()
+    assert np.array_equal(S.row_values(h.cpu().numpy(), hs.cpu().numpy()), 32 * np.repeat(u, counts, 0))
+    assert (y == 0).all()
