@@ -33,7 +33,6 @@ typedef int i32x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
 
 constexpr int kBlk = 128;                                   // elements of a scale block
-constexpr float kMaxE4m3 = 448.0f;
 
 __host__ __device__ inline int scale_blocks(int K) { return (K + kBlk - 1) / kBlk; }
 // bytes of one row of scales: a multiple of four, so that a dword holds the
@@ -401,29 +400,24 @@ template <bool GU, int BP, int BQ, int NW, bool LATE, bool ONCE>
 struct Loads {
   static constexpr int TP = BP * 8, TQ = BQ * 8;               // 16-byte chunks of a stage
   static constexpr int NIP = TP / 64 / NW;                     // instructions per wave and stage
-  static constexpr int NIQ = (TQ / 64 + NW - 1) / NW;
+  static constexpr int NIQ = TQ / 64 / NW;
   static constexpr int LOADS = NIP + NIQ;
   static constexpr uint32_t STAGE = (TP + TQ) * 16;            // bytes
-  // every wave issues the same number of loads; those past the Q tile read
-  // nothing and land behind the ring
-  static constexpr bool SPARE = NIQ * 64 * NW > TQ;
-  static_assert(NIP * 64 * NW == TP && (NIQ == 1 || NIQ % 2 == 0), "loads per wave");
+  // every wave issues the same number of loads
+  static_assert(NIP * 64 * NW == TP && NIQ * 64 * NW == TQ && (NIQ == 1 || NIQ % 2 == 0), "loads per wave");
   static_assert(NIP % 2 == 0, "the chunk a lane loads depends on its place's parity alone");
   uint32_t voffP[NIP], voffQ[NIQ];
   uint32_t leftP[2], leftQ[NIQ == 1 ? 1 : 2];   // K minus the lane's first byte, by parity of i
-  uint32_t spare;        // byte behind the ring
   const uint8_t *pbase, *qbase;
   uint32_t pbytes, qbytes;
   uint32_t ldsP, ldsQ;   // the wave's places in the ring's first stage
   int wave, lane;
 
-  __device__ __forceinline__ void init(const Fp8Args &g, int wave_, int lane_, const void *smem,
-                                       uint32_t ring) {
+  __device__ __forceinline__ void init(int wave_, int lane_, const void *smem) {
     wave = wave_;
     lane = lane_;
     ldsP = lds_addr(smem) + (uint32_t)wave * (NIP * 1024u);
     ldsQ = lds_addr(smem) + TP * 16u + (uint32_t)wave * (NIQ * 1024u);
-    spare = lds_addr(smem) + ring;
   }
   // row and byte of the chunk that a lane loads with instruction q of an operand
   __device__ __forceinline__ int row(int q) const { return 8 * q + (lane >> 3); }
@@ -457,7 +451,7 @@ struct Loads {
 #pragma unroll
     for (int i = 0; i < NIQ; ++i) {
       const int q = NIQ * wave + i;
-      const int r = SPARE && q * 8 >= BQ ? -1 : src(row(q));
+      const int r = src(row(q));
       voffQ[i] = r >= 0 ? (uint32_t)r * (uint32_t)K + chunk(q) : kOOB;
     }
 #pragma unroll
@@ -473,8 +467,7 @@ struct Loads {
       else dma16(rs, to, voff);
     } else {
       const int j = i - NIP;
-      dma16(make_rsrc(qbase + k0, max(qbytes, k0) - k0),
-            SPARE && wave * 8 >= BQ ? spare : ldsQ + buf + (uint32_t)j * 1024u,
+      dma16(make_rsrc(qbase + k0, max(qbytes, k0) - k0), ldsQ + buf + (uint32_t)j * 1024u,
             k0 < leftQ[NIQ == 1 ? 0 : j & 1] ? voffQ[j] : kOOB);
     }
   }
@@ -1028,7 +1021,7 @@ __global__ __launch_bounds__(NW * 64) void k_grouped_fp8_small(Fp8Args g) {
   static_assert(!GU || BP == 256, "a gate/up tile holds one block of 128 h");
   constexpr bool EXACT = GU && ONCE;   // bf16 products, scales applied to their sums over a stage
   static_assert((NS - 2) * L::LOADS < 64, "vmcnt range");
-  __shared__ u32x4_t smem[NS * (L::TP + L::TQ) + 64];
+  __shared__ u32x4_t smem[NS * (L::TP + L::TQ)];
   __shared__ uint32_t s_qs[kScaleChunk / 4][BQ];
   __shared__ uint32_t s_ps[kScaleChunk / 4][4];
   __shared__ float s_amax[GU ? NW : 1][GU ? BQ : 1];
@@ -1058,7 +1051,7 @@ __global__ __launch_bounds__(NW * 64) void k_grouped_fp8_small(Fp8Args g) {
   const LDS_AS char *lds = (const LDS_AS char *)smem;
   const uint32_t at0 = (uint32_t)lr * 128u + (uint32_t)((lg ^ ((lr >> 1) & 7)) * 16);
   L ld;
-  ld.init(g, wave, lane, smem, NS * L::STAGE);
+  ld.init(wave, lane, smem);
 
   auto src = [&](int r) -> int {   // row of a, -1 past the segment or for no token
     if (r >= t.qvalid) return -1;
