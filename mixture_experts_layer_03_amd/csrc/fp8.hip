@@ -267,23 +267,25 @@ constexpr uint32_t kOOB = 0x80000000u;   // at or past every resource's byte cou
 
 // 16 bytes per lane from global memory to LDS (lane l at lds + 16 l).  In
 // assembly, so that the compiler puts no waits of its own around it; the
-// kernel waits (wait_vm) before the barrier that publishes the stage.
+// kernel waits (wait_vm) before the barrier that publishes the stage.  (s_nop:
+// a load to LDS stands a wait state behind the write of M0, which the compiler
+// cannot see to in here.)
 __device__ __forceinline__ void dma16(u32x4_t rs, uint32_t lds, uint32_t voff) {
-  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                :
                : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(voff), "s"(rs)
                : "memory", "m0");
 }
 // The same for what is read once: its lines do not stay in L2.
 __device__ __forceinline__ void dma16_once(u32x4_t rs, uint32_t lds, uint32_t voff) {
-  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen nt lds"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen nt lds"
                :
                : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(voff), "s"(rs)
                : "memory", "m0");
 }
 // The same as dma16 with 4 bytes per lane (lane l at lds + 4 l).
 __device__ __forceinline__ void dma4(u32x4_t rs, uint32_t lds, uint32_t voff) {
-  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
                :
                : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(voff), "s"(rs)
                : "memory", "m0");

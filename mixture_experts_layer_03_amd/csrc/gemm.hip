@@ -94,9 +94,11 @@ constexpr uint32_t kOOB = 0x80000000u;   // an offset past any resource: reads z
 // 64 chunks land contiguously at dst (lane l at dst + 16*l).  Written as
 // inline assembly so that the compiler does not guard later LDS reads of
 // other buffers with waits for these loads; the kernel waits for them itself
-// (wait_vm_lgkm0) before the barrier that publishes a stage.
+// (wait_vm_lgkm0) before the barrier that publishes a stage.  (s_nop: a load to
+// LDS stands a wait state behind the write of M0, which the compiler cannot
+// see to in here.)
 __device__ __forceinline__ void dma16_at(u32x4_t rs, uint32_t lds, uint32_t voff) {
-  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                :
                : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(voff), "s"(rs)
                : "memory", "m0");
@@ -109,7 +111,7 @@ __device__ __forceinline__ void dma16(u32x4_t rs, u32x4_t *dst, uint32_t voff) {
 }
 // The same with 4 bytes per lane (lane l at dst + 4*l).
 __device__ __forceinline__ void dma4_at(u32x4_t rs, uint32_t lds, uint32_t voff) {
-  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
                :
                : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(voff), "s"(rs)
                : "memory", "m0");
