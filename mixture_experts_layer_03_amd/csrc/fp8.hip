@@ -264,6 +264,13 @@ __device__ __forceinline__ u32x4_t make_rsrc(const void *base, uint32_t bytes) {
                  (uint32_t)__builtin_amdgcn_readfirstlane((int)bytes), 0x00020000u};
 }
 constexpr uint32_t kOOB = 0x80000000u;   // at or past every resource's byte count
+// Bytes (fewer than 2^31) of a resource whose base has moved by `moved`.  Signed,
+// for a scalar maximum: the saturating difference is a vector instruction, and
+// a load stands five wait states behind one that writes its resource, which the
+// compiler does not keep before inline assembly.
+__device__ __forceinline__ uint32_t left_of(uint32_t bytes, uint32_t moved) {
+  return (uint32_t)max((int)(bytes - moved), 0);
+}
 
 // 16 bytes per lane from global memory to LDS (lane l at lds + 16 l).  In
 // assembly, so that the compiler puts no waits of its own around it; the
@@ -463,13 +470,13 @@ struct Loads {
   // of the ring at `buf`
   __device__ __forceinline__ void one(int i, uint32_t k0, uint32_t buf) const {
     if (i < NIP) {
-      const u32x4_t rs = make_rsrc(pbase + k0, max(pbytes, k0) - k0);
+      const u32x4_t rs = make_rsrc(pbase + k0, left_of(pbytes, k0));
       const uint32_t to = ldsP + buf + (uint32_t)i * 1024u, voff = k0 < leftP[i & 1] ? voffP[i] : kOOB;
       if (ONCE) dma16_once(rs, to, voff);
       else dma16(rs, to, voff);
     } else {
       const int j = i - NIP;
-      dma16(make_rsrc(qbase + k0, max(qbytes, k0) - k0), ldsQ + buf + (uint32_t)j * 1024u,
+      dma16(make_rsrc(qbase + k0, left_of(qbytes, k0)), ldsQ + buf + (uint32_t)j * 1024u,
             k0 < leftQ[NIQ == 1 ? 0 : j & 1] ? voffQ[j] : kOOB);
     }
   }
@@ -565,11 +572,11 @@ struct WideLoads {
   // Instruction i of P half h / of the Q rows, of the stage at byte k0 of the
   // rows, into the place of the ring at `buf`.
   __device__ __forceinline__ void p(int h, int i, uint32_t k0, uint32_t buf) const {
-    dma16(make_rsrc(pbase[h] + k0, max(pbytes[h], k0) - k0),
+    dma16(make_rsrc(pbase[h] + k0, left_of(pbytes[h], k0)),
           ldsP + buf + (uint32_t)h * HALF + (uint32_t)i * 1024u, k0 < left[i] ? voffP[i] : kOOB);
   }
   __device__ __forceinline__ void q(int i, uint32_t k0, uint32_t buf) const {
-    dma16(make_rsrc(qbase + k0, max(qbytes, k0) - k0), ldsQ + buf + (uint32_t)i * 1024u,
+    dma16(make_rsrc(qbase + k0, left_of(qbytes, k0)), ldsQ + buf + (uint32_t)i * 1024u,
           k0 < left[i & 1] ? voffQ[i] : kOOB);
   }
   // all offsets in registers here

@@ -137,7 +137,7 @@ def test_the_rules_are_found_in_a_listing():
     assert run(load, "v_readlane_b32 s4, v1, 3", "s_branch 0", "s_endpgm") == []
 
 
-@pytest.mark.parametrize("rule", ["m0"])
+@pytest.mark.parametrize("rule", ["m0", "sgpr"])
 def test_the_library_keeps_the_wait_states(kernels, rule):
     loads, bad = 0, {}
     for name, code in kernels:
