@@ -239,11 +239,11 @@ __device__ __forceinline__ int select64(const RouteArgs &g, const float *x, int 
 // sum, reciprocal: 6 units of 2^-24; the bias's sum 2^-24 |c|), for softmax
 // scores 2^-24 (2 + 40 s_max) + 2^-23 |c| (the argument's error is in
 // proportion to it, |d| exp(-|d|) < 0.4; sum and reciprocal 32 units of the
-// score).  Where the last group that stays and the first that goes are nearer
-// than that, the wave takes the groups' values in fp64; where neighbours in
-// the order are, the first k + 1 are ranked again in fp64; where that cannot
-// settle it (the k + 2nd is close too, a NaN, scores of -inf), the wave
-// selects in fp64 from the start.
+// score); a sum of two choices has the errors of both.  Where the last group
+// that stays and the first that goes are nearer than that, the wave takes the
+// groups' values in fp64; where neighbours in the order are, the first k + 1
+// are ranked again in fp64; where that cannot settle it (the k + 2nd is close
+// too, a NaN, scores of -inf), the wave selects in fp64 from the start.
 //
 // The vector units bound it, not memory: 32768 tokens x 256 experts in 8
 // groups, sigmoid, bias, top-8 take 22 us (31 at V = 4, 24 at V = 16; the
@@ -315,14 +315,21 @@ __global__ __launch_bounds__(256) void k_route_scored(RouteArgs g) {
     }
     top2(a, b, g.span);
     const float val = g.pairs ? from_key(a) + from_key(b) : from_key(a);
-    const float near = scored ? 2.0f * slack(val) : -1.0f;
+    // How near two groups' values are that fp32 cannot tell apart.  The errors of
+    // a sum are those of its addends: where they differ in sign (a bias may be
+    // of any size) they are larger than the sum by far, and any group's count.
+    float near = 2.0f * slack(val);
+    if (g.pairs && g.bias && __any(gi < g.groups && b < 0)) {
+      const float own = slack(from_key(a)) + slack(from_key(b));
+      near = reduce<G>(gi < g.groups ? own : 0.0f, Max());
+    }
     int rank = 0;
     bool close = false;   // a group behind this one, nearer than the errors
     for (int i = 0; i < g.groups; ++i) {
       const float o = __shfl(val, i * g.span, G);
       const bool before = o > val || (o == val && i < gi);
       rank += before ? 1 : 0;
-      close |= !before && i != gi && val - o <= near;
+      close |= scored && !before && i != gi && !(val - o > near);   // (sums of one infinity too)
     }
     bool kept = rank < g.keep;
     if (__any(live && gi < g.groups && rank == g.keep - 1 && close)) {
