@@ -306,8 +306,9 @@ __global__ __launch_bounds__(256) void k_route_scored(RouteArgs g) {
     if (g.pairs && !g.bias) {   // the scores' sum; a score of no expert would be 0
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const int k = to_key(g.sigmoid ? sigmoid(c[v]) : __expf(c[v] - shift) * top);
-        take(gi < g.groups && li * V + v < g.size ? k : kLowestKey);
+        const float sc = g.sigmoid ? sigmoid(c[v]) : __expf(c[v] - shift) * top;
+        unsure |= sc != sc;   // a logit of +inf: no logit is a NaN, but all scores are
+        take(gi < g.groups && li * V + v < g.size ? to_key(sc) : kLowestKey);
       }
     } else {
 #pragma unroll

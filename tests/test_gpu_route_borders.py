@@ -68,3 +68,59 @@ def test_group_sums_next_to_a_group_of_large_addends(sigmoid):
             lift = np.float32(near - s[t, g].sum())
             bias[g, 0], bias[g, 1] = 512.0 + lift, -512.0
             _compare(x[t:t + 1], bias.reshape(-1), k, sigmoid, (G, keep, 2), True, dev)
+
+
+ROWS = ["masked", "lowest", "three left", "five left", "half masked", "saturated", "small scores", "two NaN", "all NaN",
+        "tiny scores", "one infinite", "group left", "all infinite", "infinite in the last group"]
+
+
+def _special(name, E, x):
+    low = np.finfo(np.float32).min
+    if name == "masked":
+        x[:] = -np.inf
+    elif name == "lowest":
+        x[:] = low
+    elif name == "three left":
+        x[3:] = -np.inf
+    elif name == "five left":
+        x[5:] = low
+    elif name == "half masked":
+        x[::2] = -np.inf
+    elif name == "saturated":
+        x[:] = np.linspace(30, 90, E)
+    elif name == "small scores":
+        x[:] = np.linspace(-90, -30, E)
+    elif name == "two NaN":
+        x[[1, 9]] = np.nan
+    elif name == "all NaN":
+        x[:] = np.nan
+    elif name == "tiny scores":
+        x[:] = np.linspace(-300, -200, E)
+    elif name == "one infinite":
+        x[6] = np.inf
+    elif name == "group left":
+        x[:3 * E // 4] = -np.inf
+    elif name == "all infinite":
+        x[:] = np.inf
+    else:
+        x[E - 1] = np.inf
+    return x
+
+
+@pytest.mark.parametrize("sigmoid", [True, False], ids=["sigmoid", "softmax"])
+@pytest.mark.parametrize("groups", [(1, 1, 1), (4, 2, 2), (4, 2, 1), (4, 1, 2)],
+                         ids=["whole", "groups-top2", "groups-top1", "one-group"])
+@pytest.mark.parametrize("biased", [True, False], ids=["bias", "plain"])
+@pytest.mark.parametrize("name", ROWS)
+def test_special_rows_by_themselves(name, biased, groups, sigmoid):
+    """Each row alone, and behind rows that the quick path is sure of."""
+    dev = need_gpu()
+    for E, k in ((16, 4), (64, 3)):
+        x, r = _logits(9, E, 2 + E)
+        bias = (r.standard_normal(E) * 0.1).astype(np.float32) if biased else None
+        row = _special(name, E, x[1].copy())
+        for renorm in (True, False):
+            _compare(row[None], bias, k, sigmoid, groups, renorm, dev)
+            y = x[1:].copy()
+            y[5] = row
+            _compare(y, bias, k, sigmoid, groups, renorm, dev)
