@@ -3,7 +3,9 @@
 Argument marshalling only: every function here takes torch tensors that
 already live on the current HIP device, checks nothing beyond what ctypes
 needs, passes raw pointers and sizes to the function of the same name in
-libmoe.so, and raises MoeError on a non-zero status.  All arithmetic runs in
+libmoe.so, and raises MoeError on a non-zero status.  The 8-bit calls alone
+look at their operands' sizes (ValueError): rows of scales are padded, and a
+tensor without the padding would be read or written past its end.  All arithmetic runs in
 the library's kernels.  The library must have been built
 (``python -m mixture_experts_layer_03_amd.build``); there is no fallback.
 """
@@ -411,14 +413,41 @@ def moe_fp8_scale_cols(K) -> int:
     return int(lib().moe_fp8_scale_cols(K))
 
 
+def _pitch(t, cols):
+    """Whether the rows of a scale tensor are not `cols` long (a flat one has none)."""
+    return t.shape[-1] != cols and t.dim() > 1
+
+
+def _misfit(fn, *operands):
+    """Raises for the first (name, tensor, rows, cols, bytes per element) that
+    does not hold its rows; cols is given for scale tensors, whose rows are
+    padded to moe_fp8_scale_cols, and else counted into rows."""
+    for name, t, rows, cols, size in operands:
+        if t is None:
+            continue
+        need = rows * (cols or 1) * size
+        if (cols and _pitch(t, cols)) or t.nbytes < need or not t.is_contiguous():
+            raise ValueError("%s: %s must be contiguous and hold %d bytes%s, not %s of %s"
+                             % (fn, name, need, " in rows of %d" % cols if cols else "",
+                                tuple(t.shape), t.dtype))
+
+
 def moe_quant_rows_fp8(x, q, scale, stream=None):
     R, K = x.shape
+    cols = -(-K // 512) * 4
+    if (q.nbytes < R * K or _pitch(scale, cols) or scale.nbytes < R * cols
+            or not (x.is_contiguous() and q.is_contiguous() and scale.is_contiguous())):
+        _misfit("moe_quant_rows_fp8", ("x", x, 0, 0, 1), ("q", q, R * K, 0, 1),
+                ("scale", scale, R, cols, 1))
     _check("moe_quant_rows_fp8", lib().moe_quant_rows_fp8(
         _p(x), _dtype_code(x), R, K, _p(q), _p(scale), _stream(stream)))
 
 
 def moe_quant_weights_fp8(w, q, scale, qt=None, scale_t=None, stream=None):
     E, N, K = w.shape
+    _misfit("moe_quant_weights_fp8", ("w", w, 0, 0, 1), ("q", q, E * N * K, 0, 1),
+            ("scale", scale, E * -(-N // 128), -(-K // 512) * 4, 1), ("qt", qt, E * N * K, 0, 1),
+            ("scale_t", scale_t, E * -(-K // 128), -(-N // 512) * 4, 1))
     _check("moe_quant_weights_fp8", lib().moe_quant_weights_fp8(
         _p(w), _dtype_code(w), E, N, K, _p(q), _p(scale), _p(qt), _p(scale_t), _stream(stream)))
 
@@ -428,6 +457,18 @@ def moe_grouped_gemm_fp8(a, a_scale, offsets, b, b_scale, row_scale, c, row_to_s
     """With row_to_slot, a holds token rows and row r reads token row_to_slot[r] / k."""
     R = c.shape[0]
     E, N, K = b.shape
+    rows, cols, blocks = R if row_to_slot is None else R // max(k, 1), -(-K // 512) * 4, -(-N // 128)
+    if (a.nbytes < rows * K or a_scale.nbytes < rows * cols or _pitch(a_scale, cols)
+            or b_scale.nbytes < E * blocks * cols or _pitch(b_scale, cols)
+            or offsets.nbytes < 4 * E + 4 or c.nbytes < 2 * R * N
+            or (row_to_slot is not None and row_to_slot.nbytes < 4 * R)
+            or (row_scale is not None and row_scale.nbytes < 4 * R)
+            or not (a.is_contiguous() and a_scale.is_contiguous() and b.is_contiguous()
+                    and b_scale.is_contiguous() and c.is_contiguous())):
+        _misfit("moe_grouped_gemm_fp8", ("a", a, rows * K, 0, 1), ("a_scale", a_scale, rows, cols, 1),
+                ("offsets", offsets, E + 1, 0, 4), ("b", b, 0, 0, 1),
+                ("b_scale", b_scale, E * blocks, cols, 1), ("row_scale", row_scale, R, 0, 4),
+                ("c", c, R * N, 0, 2), ("row_to_slot", row_to_slot, R, 0, 4))
     _check("moe_grouped_gemm_fp8", lib().moe_grouped_gemm_fp8(
         _p(a), _p(a_scale), _p(row_to_slot), k, _p(offsets), E, R, N, K, _p(b), _p(b_scale),
         _p(row_scale), _p(c), _stream(stream)))
@@ -438,6 +479,30 @@ def moe_grouped_ffn_fwd_fp8(x, x_scale, offsets, w_gu, w_gu_scale, w_down, w_dow
     """With row_to_slot, x holds token rows and row r reads token row_to_slot[r] / k."""
     R, d = y_perm.shape
     E, _, f = w_down.shape
+    rows = R if row_to_slot is None else R // max(k, 1)
+    cols, cols_f = -(-d // 512) * 4, -(-f // 512) * 4
+    gu_blocks, blocks = -(-2 * f // 128), -(-d // 128)
+    if (x.nbytes < rows * d or x_scale.nbytes < rows * cols or _pitch(x_scale, cols)
+            or w_gu.nbytes < 2 * E * f * d or w_down.nbytes < E * d * f
+            or w_gu_scale.nbytes < E * gu_blocks * cols or _pitch(w_gu_scale, cols)
+            or w_down_scale.nbytes < E * blocks * cols_f or _pitch(w_down_scale, cols_f)
+            or h.nbytes < R * f or h_scale.nbytes < R * cols_f or _pitch(h_scale, cols_f)
+            or offsets.nbytes < 4 * E + 4 or y_perm.nbytes < 2 * R * d
+            or (row_to_slot is not None and row_to_slot.nbytes < 4 * R)
+            or (row_scale is not None and row_scale.nbytes < 4 * R)
+            or not (x.is_contiguous() and x_scale.is_contiguous() and w_gu.is_contiguous()
+                    and w_gu_scale.is_contiguous() and w_down.is_contiguous()
+                    and w_down_scale.is_contiguous() and h.is_contiguous()
+                    and h_scale.is_contiguous() and y_perm.is_contiguous())):
+        _misfit("moe_grouped_ffn_fwd_fp8", ("x", x, rows * d, 0, 1),
+                ("x_scale", x_scale, rows, cols, 1), ("offsets", offsets, E + 1, 0, 4),
+                ("w_gu", w_gu, 2 * E * f * d, 0, 1),
+                ("w_gu_scale", w_gu_scale, E * gu_blocks, cols, 1),
+                ("w_down", w_down, E * d * f, 0, 1),
+                ("w_down_scale", w_down_scale, E * blocks, cols_f, 1),
+                ("row_scale", row_scale, R, 0, 4), ("h", h, R * f, 0, 1),
+                ("h_scale", h_scale, R, cols_f, 1), ("y_perm", y_perm, R * d, 0, 2),
+                ("row_to_slot", row_to_slot, R, 0, 4))
     _check("moe_grouped_ffn_fwd_fp8", lib().moe_grouped_ffn_fwd_fp8(
         _p(x), _p(x_scale), _p(row_to_slot), k, _p(offsets), E, R, d, f, _p(w_gu),
         _p(w_gu_scale), _p(w_down), _p(w_down_scale), _p(row_scale), _p(h), _p(h_scale),
