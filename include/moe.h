@@ -521,9 +521,14 @@ int moe_route_scored_bwd(const float *logits, const int32_t *topk_idx, const flo
  * multiples of 16 from 16 to 65536; 1 <= E <= 1024; R < 2^31; pointers
  * 16-byte aligned.  Products accumulate in fp32, after the matrix
  * instruction has added each 8 consecutive k with at least 13 bits below the
- * largest of their products.  Rows at or past offsets[E]
- * are not read and not written.  Offsets that are no ascending sequence in
- * [0,R] are clamped to it and give unspecified rows.
+ * largest of their products (the gate/up product of few rows per expert adds
+ * them whole).  R, E and the sizes decide which kernel forms a product, and with
+ * it the order of these sums: a row's result depends on its own values and on
+ * those sizes, and on no other row.  Launches of another R or E, an expert
+ * split among several included, may differ in it by the sums' errors, and where
+ * such a sum is rounded to 8 bits (h) by a step of e4m3.  Rows at or past
+ * offsets[E] are not read and not written.  Offsets that are no ascending
+ * sequence in [0,R] are clamped to it and give unspecified rows.
  */
 int moe_fp8_scale_cols(int K);
 
