@@ -1,8 +1,8 @@
 """GPU parity of the 8-bit products at the sizes where each of their kernels runs.
 
-The kernel of big tiles takes products of more than 32 to 48 rows an expert whose
-small tiles do not all run at once: here many output columns reach it with few
-rows, so that the ragged ends of its tiles (rows, columns, K, experts) are
+The kernel of big tiles takes products of more than 32 rows an expert (gate/up: 20)
+whose small tiles do not all run at once: here many output columns reach it with
+few rows, so that the ragged ends of its tiles (rows, columns, K, experts) are
 cheap to cover.  Bounds are those of tests/test_gpu_fp8.py.
 """
 import numpy as np
