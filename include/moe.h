@@ -443,6 +443,8 @@ size_t moe_aux_loss_workspace_size(int64_t T, int E);
  * with the same n_valid; aux_out: [2] fp32 (out); d_logits: [T,E] fp32 (in/out)
  * or NULL; coeff must be finite.  Deterministic: per-block partial sums
  * combined in a fixed order.  ws: moe_aux_loss_workspace_size(T,E) bytes.
+ * (Beside moe_route_scored with sigmoid scores this is not the loss of the
+ * router's own scores.)
  */
 int moe_aux_loss(const float *logits, const int32_t *load, int64_t T, int64_t n_valid, int E,
                  int k, float coeff, float *aux_out, float *d_logits, void *ws, size_t ws_bytes,

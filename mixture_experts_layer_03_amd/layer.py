@@ -265,8 +265,12 @@ class MoEBlock:
                  n_valid: Optional[int] = None, lora=None):
         """aux_coeff != 0 adds the load-balancing auxiliary loss's gradient to
         the router's; its statistics (and self.aux = [aux, aux_scaled]) cover
-        the first n_valid tokens (all if None)."""
+        the first n_valid tokens (all if None).  Its probabilities are the
+        softmax over all experts, so a router of sigmoid scores refuses it."""
         assert self.has_bwd
+        if aux_coeff != 0.0 and self.router is not None and self.router.score != "softmax":
+            raise ValueError("aux_coeff: the auxiliary loss is defined on softmax probabilities, "
+                             "not on a router's sigmoid scores")
         if not self.gather:
             abi.moe_combine_bwd(dy, self.slot_to_row, self.k, self.dy_perm, stream)
         self.experts_backward(w_gu, w_down, stream, lora, x=x, dy=dy)
