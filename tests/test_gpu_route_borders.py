@@ -124,3 +124,26 @@ def test_special_rows_by_themselves(name, biased, groups, sigmoid):
             y = x[1:].copy()
             y[5] = row
             _compare(y, bias, k, sigmoid, groups, renorm, dev)
+
+
+# E, k, n_group, topk_group, group_top: with more than 2048 tokens a lane holds up to 8 experts and a token 8 to 64 lanes
+MANY = [(64, 4, 1, 1, 1), (128, 8, 1, 1, 1), (256, 8, 8, 4, 2), (256, 6, 8, 3, 1), (160, 6, 8, 3, 2), (24, 2, 3, 1, 2),
+        (512, 10, 1, 1, 1), (1020, 9, 17, 5, 2), (37, 32, 1, 1, 1)]
+
+
+@pytest.mark.parametrize("sigmoid", [True, False], ids=["sigmoid", "softmax"])
+@pytest.mark.parametrize("biased", [True, False], ids=["bias", "plain"])
+@pytest.mark.parametrize("case", MANY, ids=["E%d-k%d-g%d-%d-top%d" % c for c in MANY])
+def test_more_than_2048_tokens(case, biased, sigmoid):
+    """The same rows as in launches of fewer, special ones among them, over the last block's end."""
+    dev = need_gpu()
+    E, k, ng, tg, gt = case
+    T = 2049 + E % 7
+    x, r = _logits(T, E, 7 * E + k)
+    for i, name in enumerate(ROWS):
+        if E > 9:
+            x[100 * i + 3] = _special(name, E, x[100 * i + 3].copy())
+    x[1600:1700] = (1 + r.standard_normal((100, E)) * 3e-3).astype(np.float32)
+    bias = (r.standard_normal(E) * (0.1 if E % 8 else 64.0)).astype(np.float32) if biased else None
+    for renorm in (True, False):
+        _compare(x, bias, k, sigmoid, (ng, tg, gt), renorm, dev)
