@@ -584,6 +584,143 @@ int moe_grouped_ffn_fwd_fp8(const uint8_t *x, const uint8_t *x_scale, const int3
                             const float *row_scale, uint8_t *h, uint8_t *h_scale, void *y_perm,
                             void *stream);
 
+/* ---------------------------------------------------------------- around the block */
+
+/*
+ * The residual stream around a block: the norm of the block's output, its
+ * gate, the scaled residual, and the norm before the next block, in one pass.
+ * With r(v) = (mean over the row of v^2 + eps)^-1/2, over each row t:
+ *   p      = y r(y) w_post                         (y where w_post is NULL)
+ *   out    = store(res_scale x + gate p)           (x NULL: gate p)
+ *   n      = store(out r(out) w_pre)               (w_pre NULL: not formed)
+ * in fp32; the second norm is of the stored out, which is all that a backward
+ * has.  y NULL: n = store(x r(x) w_pre) alone, and out, w_post and gate are
+ * NULL, res_scale 1.
+ * x, y, out, n: [T,d] (dtype); w_post, w_pre: [d] (dtype); gate by gate_kind:
+ * MOE_GATE_NONE NULL, _CHANNEL [d] (dtype), _TOKEN [T] fp32, _ELEMENT [T,d]
+ * (dtype).  rstd_post, rstd_pre: [T] fp32, r(y) and r(out) (out, or NULL).
+ * out may be x, n may be y; else no two tensors may overlap.  d a multiple of
+ * 8, at most 16384; T below 2^26, and T times the row's waves (up to 16) below
+ * 2^26 too.
+ */
+#define MOE_GATE_NONE    0
+#define MOE_GATE_CHANNEL 1
+#define MOE_GATE_TOKEN   2
+#define MOE_GATE_ELEMENT 3
+int moe_residual_norm(const void *x, const void *y, const void *gate, int gate_kind,
+                      const void *w_post, const void *w_pre, float res_scale, float eps, int dtype,
+                      int64_t T, int d, void *out, void *n, float *rstd_post, float *rstd_pre,
+                      void *stream);
+
+/*
+ * Gradient of moe_residual_norm.  d_out: [T,d], the gradient that reaches out
+ * by the stream (NULL: none); d_n: [T,d], that of n (NULL exactly where w_pre
+ * is); out, y, gate, w_post, w_pre, rstd_post, rstd_pre, res_scale as the
+ * forward had or gave them (out is read for w_pre only, y for w_post or
+ * d_gate only).  With D the whole gradient of out:
+ *   D   = d_out + rn (q - out rn^2 mean(q out)),  q = d_n w_pre, rn = rstd_pre
+ *   d_x = store(res_scale D),   P = gate D
+ *   d_y = store(rp (P w_post - y rp^2 mean(P w_post y))), rp = rstd_post (P without w_post)
+ *   d_w_pre = sum_t d_n out rn,  d_w_post = sum_t P y rp,      [d] fp32
+ *   d_gate  = D p, summed over what the gate is shared by: [d] fp32, [T] fp32
+ *             or [T,d] (dtype)
+ * Each output may be NULL.  After moe_residual_norm with y NULL: out is its x,
+ * y, gate and w_post are NULL and d_x is the gradient.  d_x may be d_out; else
+ * no output may overlap another tensor.  Sums over t are formed in a fixed
+ * order.  T = 0 gives zero weight gradients.  ws:
+ * moe_residual_norm_bwd_workspace_size(T,d) bytes, needed for d_w_pre,
+ * d_w_post and a channel gate's gradient (MOE_ERR_WORKSPACE if smaller).
+ */
+size_t moe_residual_norm_bwd_workspace_size(int64_t T, int d);
+int moe_residual_norm_bwd(const void *d_out, const void *d_n, const void *out, const void *y,
+                          const void *gate, int gate_kind, const void *w_post, const void *w_pre,
+                          const float *rstd_post, const float *rstd_pre, float res_scale, int dtype,
+                          int64_t T, int d, void *d_x, void *d_y, float *d_w_post, float *d_w_pre,
+                          void *d_gate, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * moe_combine with the weights applied where the rows come back ("weighted by
+ * the top-k probabilities", EP token-routing figure), for expert rows that do
+ * not carry them yet (row_scale NULL in the expert calls):
+ *   y[t] = store(sum over j ascending, an fp32 fma chain from +0, of
+ *                weights[t*k+j] y_perm[slot_to_row[t*k+j]])
+ * A negative slot_to_row entry has no row and adds nothing; what y_perm holds
+ * for rows that no slot names is not read.  weights: [T,k] fp32, by slot.
+ */
+int moe_combine_weighted(const void *y_perm, const int32_t *slot_to_row, const float *weights,
+                         int dtype, int64_t T, int d, int k, void *y, void *stream);
+
+/*
+ * Gradient of moe_combine_weighted: for every slot s = t*k+j that has a row r,
+ *   dy_perm[r] = store(weights[s] dy[t]),   d_row_scale[r] = <dy[t], y_perm[r]>
+ * by row, as moe_route_bwd and moe_route_scored_bwd read it.  Rows that no
+ * slot names are left as they were.  dy_perm or d_row_scale may be NULL, y_perm too
+ * where d_row_scale is; dy_perm may not overlap y_perm.  No two slots may
+ * name the same row.  T*k below 2^26.
+ */
+int moe_combine_weighted_bwd(const void *dy, const void *y_perm, const int32_t *slot_to_row,
+                             const float *weights, int dtype, int64_t T, int d, int k,
+                             void *dy_perm, float *d_row_scale, void *stream);
+
+/*
+ * moe_combine_weighted (weights NULL: moe_combine) and moe_residual_norm on
+ * its rows in one pass, bit for bit what the two calls give: y, the combined
+ * rows [T,d], is stored for a backward, or NULL.  Arguments and errors as
+ * theirs; y may not overlap another tensor.
+ */
+int moe_combine_residual_norm(const void *y_perm, const int32_t *slot_to_row, const float *weights,
+                              int k, const void *x, const void *gate, int gate_kind,
+                              const void *w_post, const void *w_pre, float res_scale, float eps,
+                              int dtype, int64_t T, int d, void *y, void *out, void *n,
+                              float *rstd_post, float *rstd_pre, void *stream);
+
+/* ---------------------------------------------------------------- optimizer */
+
+/*
+ * One AdamW step over n tensors (the pages' trainer keeps bf16 weights with
+ * stochastic rounding and identically seeded random numbers: "Halo:
+ * Frontier-Lab Training for Everyone").  For each element, in fp32, each
+ * operation rounded by itself, g = grad * grad_scale[0] (1 if NULL):
+ *   m = beta1 m + (1-beta1) g,   v = beta2 v + ((1-beta2) g) g
+ *   p = p (1 - lr weight_decay) - lr/(1-beta1^step) m / (sqrt(v)/sqrt(1-beta2^step) + eps)
+ * (root and reciprocal to 1 ulp).  param: param_dtype; grad: grad_dtype, fp32
+ * or, for bf16 parameters, bf16.  A bf16 parameter has a 32-bit copy `master`,
+ * which is what is stepped and then rounded to nearest, or (all tensors of a
+ * call alike) none; then p is rounded at random between its two bf16
+ * neighbours, the upper with the probability of p's place between them.
+ * State: state_bits 32: m, v [numel] fp32.  8: m [numel] e4m3, v [numel] e5m2,
+ * and a power of two 2^s for each 128 elements, m_scale and v_scale
+ * [ceil(numel/128)], the byte s + 127: s >= -126 the smallest with the block's
+ * largest finite magnitude <= 448 2^s (m) or 57344 2^s (v).  Both are rounded
+ * at random like p, with 16 random bits; a v that is not zero is at least the
+ * smallest code, since its root divides.  NaN and infinities become 0x7f.
+ * Zero bytes with scale bytes of 127 are the state before the first step.
+ * Random bits: with mix(a): a ^= a >> 16, a *= 0x971cbef1, a ^= a >> 15,
+ * a *= 0x6a695495, a ^= a >> 16 (32 bits),
+ *   key = mix(mix(mix(mix(seed & 0xffffffff) ^ seed >> 32) ^ step) ^ i) ^ (e >> 32)
+ *   r   = mix(key ^ (e & 0xffffffff)) for element e of tensors[i];
+ * p takes r's low half, m its high half, v the high half of r * 0x30e9132d.
+ * step: 1, 2, ... below 2^32.  lr_dev (fp32) and step_dev (int64), both or
+ * neither: the learning rate and the step count are read from the device, for
+ * a captured step; lr and step are not used, and 1-beta^step is formed in fp32.
+ * tensors: a HOST array, read before the call returns.  Tensors with numel 0
+ * are skipped; a param, master, m or v that is listed twice is refused, and no
+ * two may overlap.  param, grad, master, m, v 16-byte aligned.
+ */
+typedef struct moe_adamw_tensor {
+  void *param;
+  const void *grad;
+  float *master;
+  void *m, *v;
+  uint8_t *m_scale, *v_scale;
+  int64_t numel;
+  double weight_decay;
+} moe_adamw_tensor;
+int moe_adamw_step(const moe_adamw_tensor *tensors, int n, int param_dtype, int grad_dtype,
+                   int state_bits, double lr, double beta1, double beta2, double eps, int64_t step,
+                   uint64_t seed, const float *grad_scale, const float *lr_dev,
+                   const int64_t *step_dev, void *stream);
+
 /* ---------------------------------------------------------------- timing */
 
 /*

@@ -3,9 +3,11 @@
 Argument marshalling only: every function here takes torch tensors that
 already live on the current HIP device, checks nothing beyond what ctypes
 needs, passes raw pointers and sizes to the function of the same name in
-libmoe.so, and raises MoeError on a non-zero status.  The 8-bit calls alone
+libmoe.so, and raises MoeError on a non-zero status.  The 8-bit calls
 look at their operands' sizes (ValueError): rows of scales are padded, and a
-tensor without the padding would be read or written past its end.  All arithmetic runs in
+tensor without the padding would be read or written past its end.  The residual
+norms and the weighted combine look at shapes, types, strides and devices
+(ValueError), since an optional tensor is easily given in another's place.  All arithmetic runs in
 the library's kernels.  The library must have been built
 (``python -m mixture_experts_layer_03_amd.build``); there is no fallback.
 """
@@ -24,6 +26,7 @@ MOE_F32 = 0
 MOE_BF16 = 1
 MOE_SCORE_SOFTMAX = 0
 MOE_SCORE_SIGMOID = 1
+MOE_GATE_NONE, MOE_GATE_CHANNEL, MOE_GATE_TOKEN, MOE_GATE_ELEMENT = 0, 1, 2, 3
 
 _c_void_p = ctypes.c_void_p
 _i32, _i64, _sz = ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
@@ -111,6 +114,25 @@ _SIGS = {
                                        _i64, _i32, _i32, _c_void_p, _c_void_p, _c_void_p,
                                        _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
                                        _c_void_p]),
+    "moe_residual_norm": (_i32, [_c_void_p, _c_void_p, _c_void_p, _i32, _c_void_p, _c_void_p,
+                                 ctypes.c_float, ctypes.c_float, _i32, _i64, _i32, _c_void_p,
+                                 _c_void_p, _c_void_p, _c_void_p, _c_void_p]),
+    "moe_residual_norm_bwd_workspace_size": (_sz, [_i64, _i32]),
+    "moe_residual_norm_bwd": (_i32, [_c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _i32,
+                                     _c_void_p, _c_void_p, _c_void_p, _c_void_p, ctypes.c_float,
+                                     _i32, _i64, _i32, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
+                                     _c_void_p, _c_void_p, _sz, _c_void_p]),
+    "moe_combine_weighted": (_i32, [_c_void_p, _c_void_p, _c_void_p, _i32, _i64, _i32, _i32,
+                                    _c_void_p, _c_void_p]),
+    "moe_combine_weighted_bwd": (_i32, [_c_void_p, _c_void_p, _c_void_p, _c_void_p, _i32, _i64,
+                                        _i32, _i32, _c_void_p, _c_void_p, _c_void_p]),
+    "moe_combine_residual_norm": (_i32, [_c_void_p, _c_void_p, _c_void_p, _i32, _c_void_p,
+                                         _c_void_p, _i32, _c_void_p, _c_void_p, ctypes.c_float,
+                                         ctypes.c_float, _i32, _i64, _i32, _c_void_p, _c_void_p,
+                                         _c_void_p, _c_void_p, _c_void_p, _c_void_p]),
+    "moe_adamw_step": (_i32, [_c_void_p, _i32, _i32, _i32, _i32, ctypes.c_double, ctypes.c_double,
+                              ctypes.c_double, ctypes.c_double, _i64, ctypes.c_uint64, _c_void_p,
+                              _c_void_p, _c_void_p, _c_void_p]),
     "moe_timing_enable": (_i32, [_i32]),
     "moe_timing_reset": (_i32, []),
     "moe_timing_query": (_i32, [ctypes.c_char_p, ctypes.POINTER(ctypes.c_double),
@@ -507,6 +529,142 @@ def moe_grouped_ffn_fwd_fp8(x, x_scale, offsets, w_gu, w_gu_scale, w_down, w_dow
         _p(x), _p(x_scale), _p(row_to_slot), k, _p(offsets), E, R, d, f, _p(w_gu),
         _p(w_gu_scale), _p(w_down), _p(w_down_scale), _p(row_scale), _p(h), _p(h_scale),
         _p(y_perm), _stream(stream)))
+
+
+def _fits(fn, *operands):
+    """Raises for the first (name, tensor, shape, dtype) that is not a contiguous tensor of that
+    shape and type on the current device; None passes."""
+    import torch
+    here = None
+    for name, t, shape, dtype in operands:
+        if t is None:
+            continue
+        if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
+            raise ValueError("%s: %s must be a contiguous %s of %s, not %s of %s%s"
+                             % (fn, name, tuple(shape), dtype, tuple(t.shape), t.dtype,
+                                "" if t.is_contiguous() else " with strides"))
+        at = t.get_device()
+        if here is None:
+            here = torch.cuda.current_device() if at >= 0 else 0
+        if at != here:
+            raise ValueError("%s: %s is on %s, not on the current device" % (fn, name, t.device))
+
+
+def _gate_kind(fn, gate, T, d, dtype):
+    """(kind, shape, type) of a gate by its shape: [d] a channel's, [T,1] a token's (fp32), [T,d]."""
+    import torch
+    if gate is None:
+        return MOE_GATE_NONE, None, None
+    if gate.shape == (d,):
+        return MOE_GATE_CHANNEL, (d,), dtype
+    if gate.shape == (T, 1):
+        return MOE_GATE_TOKEN, (T, 1), torch.float32
+    if gate.shape == (T, d):
+        return MOE_GATE_ELEMENT, (T, d), dtype
+    raise ValueError("%s: gate must be [d], [T,1] or [T,d], not %s" % (fn, tuple(gate.shape)))
+
+
+def moe_residual_norm(x, y, out, n, w_post=None, w_pre=None, gate=None, res_scale=1.0, eps=1e-6,
+                      rstd_post=None, rstd_pre=None, stream=None):
+    """y None: n alone, the norm of x.  gate: [d], [T,1] (fp32) or [T,d]."""
+    import torch
+    fn, some = "moe_residual_norm", x if y is None else y
+    dt = some.dtype
+    T, d = some.shape
+    kind, gshape, gtype = _gate_kind(fn, gate, T, d, dt)
+    row, f32 = (T, d), torch.float32
+    _fits(fn, ("x", x, row, dt), ("y", y, row, dt), ("out", out, row, dt), ("n", n, row, dt),
+          ("w_post", w_post, (d,), dt), ("w_pre", w_pre, (d,), dt), ("gate", gate, gshape, gtype),
+          ("rstd_post", rstd_post, (T,), f32), ("rstd_pre", rstd_pre, (T,), f32))
+    _check(fn, lib().moe_residual_norm(
+        _p(x), _p(y), _p(gate), kind, _p(w_post), _p(w_pre), res_scale, eps, _dtype_code(some), T, d,
+        _p(out), _p(n), _p(rstd_post), _p(rstd_pre), _stream(stream)))
+
+
+def moe_residual_norm_bwd_workspace_size(T, d) -> int:
+    return int(lib().moe_residual_norm_bwd_workspace_size(T, d))
+
+
+def moe_residual_norm_bwd(d_out, d_n, out, y, d_x, d_y, ws, w_post=None, w_pre=None, gate=None,
+                          res_scale=1.0, rstd_post=None, rstd_pre=None, d_w_post=None,
+                          d_w_pre=None, d_gate=None, stream=None):
+    import torch
+    fn, some = "moe_residual_norm_bwd", d_n if d_out is None else d_out
+    dt = some.dtype
+    T, d = some.shape
+    kind, gshape, gtype = _gate_kind(fn, gate, T, d, dt)
+    row, f32 = (T, d), torch.float32
+    _fits(fn, ("d_out", d_out, row, dt), ("d_n", d_n, row, dt), ("out", out, row, dt),
+          ("y", y, row, dt), ("d_x", d_x, row, dt), ("d_y", d_y, row, dt),
+          ("w_post", w_post, (d,), dt), ("w_pre", w_pre, (d,), dt), ("gate", gate, gshape, gtype),
+          ("rstd_post", rstd_post, (T,), f32), ("rstd_pre", rstd_pre, (T,), f32),
+          ("d_w_post", d_w_post, (d,), f32), ("d_w_pre", d_w_pre, (d,), f32),
+          ("d_gate", d_gate, gshape, f32 if kind == MOE_GATE_CHANNEL else gtype))
+    _check(fn, lib().moe_residual_norm_bwd(
+        _p(d_out), _p(d_n), _p(out), _p(y), _p(gate), kind, _p(w_post), _p(w_pre), _p(rstd_post),
+        _p(rstd_pre), res_scale, _dtype_code(some), T, d, _p(d_x), _p(d_y), _p(d_w_post),
+        _p(d_w_pre), _p(d_gate), _p(ws), 0 if ws is None else ws.nbytes, _stream(stream)))
+
+
+def moe_combine_weighted(y_perm, slot_to_row, weights, y, stream=None):
+    import torch
+    fn = "moe_combine_weighted"
+    T, k = weights.shape
+    d = y.shape[1]
+    _fits(fn, ("y_perm", y_perm, (y_perm.shape[0], d), y.dtype), ("y", y, (T, d), y.dtype),
+          ("slot_to_row", slot_to_row, (T * k,), torch.int32), ("weights", weights, (T, k), torch.float32))
+    _check(fn, lib().moe_combine_weighted(_p(y_perm), _p(slot_to_row), _p(weights), _dtype_code(y),
+                                          T, d, k, _p(y), _stream(stream)))
+
+
+def moe_combine_weighted_bwd(dy, y_perm, slot_to_row, weights, dy_perm, d_row_scale, stream=None):
+    import torch
+    fn = "moe_combine_weighted_bwd"
+    T, k = weights.shape
+    d = dy.shape[1]
+    R = dy_perm.shape[0] if y_perm is None else y_perm.shape[0]
+    _fits(fn, ("dy", dy, (T, d), dy.dtype), ("y_perm", y_perm, (R, d), dy.dtype),
+          ("slot_to_row", slot_to_row, (T * k,), torch.int32),
+          ("weights", weights, (T, k), torch.float32), ("dy_perm", dy_perm, (R, d), dy.dtype),
+          ("d_row_scale", d_row_scale, (R,), torch.float32))
+    _check(fn, lib().moe_combine_weighted_bwd(
+        _p(dy), _p(y_perm), _p(slot_to_row), _p(weights), _dtype_code(dy), T, d, k, _p(dy_perm),
+        _p(d_row_scale), _stream(stream)))
+
+
+def moe_combine_residual_norm(y_perm, slot_to_row, weights, k, x, out, n, y=None, w_post=None,
+                              w_pre=None, gate=None, res_scale=1.0, eps=1e-6, rstd_post=None,
+                              rstd_pre=None, stream=None):
+    """weights None: the rows carry them already.  y: the combined rows, stored for a backward."""
+    import torch
+    fn, dt = "moe_combine_residual_norm", out.dtype
+    T, d = out.shape
+    kind, gshape, gtype = _gate_kind(fn, gate, T, d, dt)
+    row, f32 = (T, d), torch.float32
+    _fits(fn, ("y_perm", y_perm, (y_perm.shape[0], d), dt),
+          ("slot_to_row", slot_to_row, (T * k,), torch.int32), ("weights", weights, (T, k), f32),
+          ("x", x, row, dt), ("y", y, row, dt), ("out", out, row, dt), ("n", n, row, dt),
+          ("w_post", w_post, (d,), dt), ("w_pre", w_pre, (d,), dt), ("gate", gate, gshape, gtype),
+          ("rstd_post", rstd_post, (T,), f32), ("rstd_pre", rstd_pre, (T,), f32))
+    _check(fn, lib().moe_combine_residual_norm(
+        _p(y_perm), _p(slot_to_row), _p(weights), k, _p(x), _p(gate), kind, _p(w_post), _p(w_pre),
+        res_scale, eps, _dtype_code(out), T, d, _p(y), _p(out), _p(n), _p(rstd_post), _p(rstd_pre),
+        _stream(stream)))
+
+
+class AdamwTensor(ctypes.Structure):
+    """moe_adamw_tensor"""
+    _fields_ = [("param", _c_void_p), ("grad", _c_void_p), ("master", _c_void_p), ("m", _c_void_p),
+                ("v", _c_void_p), ("m_scale", _c_void_p), ("v_scale", _c_void_p), ("numel", _i64),
+                ("weight_decay", ctypes.c_double)]
+
+
+def moe_adamw_step(tensors, n, param_dtype, grad_dtype, state_bits, lr, beta1, beta2, eps, step,
+                   seed, grad_scale=None, lr_dev=None, step_dev=None, stream=None):
+    """tensors: a ctypes array of n AdamwTensor."""
+    _check("moe_adamw_step", lib().moe_adamw_step(
+        ctypes.addressof(tensors), n, param_dtype, grad_dtype, state_bits, lr, beta1, beta2, eps,
+        step, seed, _p(grad_scale), _p(lr_dev), _p(step_dev), _stream(stream)))
 
 
 def moe_timing_enable(on: bool):

@@ -1,0 +1,183 @@
+// Expert rows back to their tokens with the combine weights applied here (the
+// rows are "weighted by the top-k probabilities" where they return: "Halo's
+// 2.8x over TRL is not a kernel, and its own benchmark proves it", section
+// "Where the gap actually is"), and the gradient, written as gathers with no
+// atomic adds.
+//   y[t] = store(sum_j w[t,j] y_perm[row(t,j)])
+//   dy_perm[row(t,j)] = store(w[t,j] dy[t]),  d_row_scale[row(t,j)] = <dy[t], y_perm[row(t,j)]>
+// Both move each row once and compute 2 to 3 operations an element: HBM bounds them.
+#include "rows.h"
+
+namespace moe {
+namespace {
+
+// One wave for 128 16-byte pieces of a token's row, four expert rows in flight.
+constexpr int kPieces = 2;
+template <typename T>
+__global__ __launch_bounds__(256) void k_combine_weighted(const T *__restrict__ y_perm,
+                                                          const int32_t *__restrict__ slot_to_row,
+                                                          const float *__restrict__ w, int64_t ntok,
+                                                          int d, int k, T *__restrict__ y) {
+  constexpr int N = kVec<T>;
+  const int nvec = d / N, parts = (nvec + 64 * kPieces - 1) / (64 * kPieces);
+  const int64_t wid = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int64_t t = wid / parts;
+  if (t >= ntok) return;
+  const int lane = threadIdx.x & 63;
+  const int c0 = (int)(wid - t * parts) * 64 * kPieces + lane;
+  const int myr = lane < k ? slot_to_row[t * k + lane] : -1;   // k <= 32
+  const float myw = lane < k ? w[t * k + lane] : 0.0f;
+  const u32x4_t zero = {0u, 0u, 0u, 0u};
+  float acc[kPieces][N];
+#pragma unroll
+  for (int h = 0; h < kPieces; ++h)
+#pragma unroll
+    for (int i = 0; i < N; ++i) acc[h][i] = 0.0f;
+  for (int j = 0; j < k; j += 4) {
+    u32x4_t v[4][kPieces];
+    int r[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      r[u] = j + u < k ? __builtin_amdgcn_readlane(myr, j + u) : -1;
+      const u32x4_t *row = reinterpret_cast<const u32x4_t *>(y_perm + (int64_t)max(r[u], 0) * d);
+#pragma unroll
+      for (int h = 0; h < kPieces; ++h) v[u][h] = r[u] >= 0 && c0 + 64 * h < nvec ? row[c0 + 64 * h] : zero;
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (r[u] < 0) continue;
+      const float wj = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(myw), j + u));
+#pragma unroll
+      for (int h = 0; h < kPieces; ++h) {
+        float f[N];
+        unpack(v[u][h], f, (const T *)nullptr);
+#pragma unroll
+        for (int i = 0; i < N; ++i) acc[h][i] = fmaf(wj, f[i], acc[h][i]);
+      }
+    }
+  }
+  u32x4_t *o = reinterpret_cast<u32x4_t *>(y + t * d);
+#pragma unroll
+  for (int h = 0; h < kPieces; ++h)
+    if (c0 + 64 * h < nvec) o[c0 + 64 * h] = pack(acc[h], (const T *)nullptr);
+}
+
+// One wave for each slot; the waves of a token's slots lie next to each other,
+// so that its row of dy comes from HBM once.
+constexpr int kSteps = 3;   // 16-byte pieces of a row that a lane has in flight
+template <typename T>
+__global__ __launch_bounds__(256) void k_combine_weighted_bwd(
+    const T *__restrict__ dy, const T *__restrict__ y_perm, const int32_t *__restrict__ slot_to_row,
+    const float *__restrict__ w, int64_t nslot, int d, int k, T *__restrict__ dy_perm,
+    float *__restrict__ d_row_scale) {
+  constexpr int N = kVec<T>;
+  const int nvec = d / N;
+  const int64_t slot = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  if (slot >= nslot) return;
+  const int r = slot_to_row[slot];
+  if (r < 0) return;
+  const float wj = w[slot];
+  const int lane = threadIdx.x & 63;
+  const int64_t t = (int64_t)((uint32_t)slot / (uint32_t)k);   // slots are below 2^31
+  const u32x4_t *g = reinterpret_cast<const u32x4_t *>(dy + t * d);
+  const u32x4_t *yr = reinterpret_cast<const u32x4_t *>(y_perm + (int64_t)r * d);
+  u32x4_t *o = reinterpret_cast<u32x4_t *>(dy_perm + (int64_t)r * d);
+  const u32x4_t zero = {0u, 0u, 0u, 0u};
+  float dot = 0.0f;
+  for (int c = lane; c < nvec; c += 64 * kSteps) {
+    u32x4_t a[kSteps], b[kSteps];
+#pragma unroll
+    for (int h = 0; h < kSteps; ++h) {
+      const bool ok = c + 64 * h < nvec;
+      a[h] = ok ? g[c + 64 * h] : zero;
+      b[h] = ok && d_row_scale ? yr[c + 64 * h] : zero;
+    }
+#pragma unroll
+    for (int h = 0; h < kSteps; ++h) {
+      float f[N], q[N];
+      unpack(a[h], f, (const T *)nullptr);
+      unpack(b[h], q, (const T *)nullptr);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        dot = fmaf(f[i], q[i], dot);
+        f[i] *= wj;
+      }
+      if (dy_perm && c + 64 * h < nvec) o[c + 64 * h] = pack(f, (const T *)nullptr);
+    }
+  }
+  if (!d_row_scale) return;
+  dot = wave_sum(dot);
+  if (lane == 0) d_row_scale[r] = dot;
+}
+
+int check(const char *fn, int64_t T, int d, int k, int dtype) {
+  MOE_REQUIRE(T >= 0, MOE_ERR_INVALID_ARG, "%s: T < 0", fn);
+  MOE_REQUIRE(d > 0 && d % 8 == 0, MOE_ERR_UNSUPPORTED, "%s: d=%d not a positive multiple of 8", fn, d);
+  MOE_REQUIRE(k >= 1 && k <= kMaxTopK, MOE_ERR_UNSUPPORTED, "%s: k=%d", fn, k);
+  MOE_REQUIRE(T < ((int64_t)1 << 31) / k, MOE_ERR_UNSUPPORTED, "%s: T*k >= 2^31", fn);
+  MOE_REQUIRE(dtype == MOE_BF16 || dtype == MOE_F32, MOE_ERR_UNSUPPORTED, "%s: dtype %d", fn, dtype);
+  return MOE_OK;
+}
+
+}  // namespace
+}  // namespace moe
+
+extern "C" {
+
+int moe_combine_weighted(const void *y_perm, const int32_t *slot_to_row, const float *weights,
+                         int dtype, int64_t T, int d, int k, void *y, void *stream) {
+  using namespace moe;
+  const char *fn = "moe_combine_weighted";
+  clear_error();
+  const int rc = check(fn, T, d, k, dtype);
+  if (rc != MOE_OK) return rc;
+  if (T == 0) return MOE_OK;
+  MOE_REQUIRE(y_perm && slot_to_row && weights && y, MOE_ERR_INVALID_ARG, "%s: null pointer", fn);
+  MOE_REQUIRE(aligned16(y_perm) && aligned16(y), MOE_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", fn);
+  const int64_t nvec = (int64_t)d * (dtype == MOE_BF16 ? 2 : 4) / 16;
+  const int64_t blocks = (T * ((nvec + 64 * kPieces - 1) / (64 * kPieces)) + 3) / 4;
+  MOE_REQUIRE(blocks < ((int64_t)1 << 24), MOE_ERR_UNSUPPORTED, "%s: too many tokens (T=%lld d=%d)",
+              fn, (long long)T, d);   // a launch has below 2^32 threads
+  hipStream_t s = (hipStream_t)stream;
+  MOE_LAUNCH("combine_weighted", s, {
+    if (dtype == MOE_BF16)
+      k_combine_weighted<bf16_t><<<(unsigned)blocks, 256, 0, s>>>(
+          (const bf16_t *)y_perm, slot_to_row, weights, T, d, k, (bf16_t *)y);
+    else
+      k_combine_weighted<float><<<(unsigned)blocks, 256, 0, s>>>(
+          (const float *)y_perm, slot_to_row, weights, T, d, k, (float *)y);
+  });
+  return check_launch(fn);
+}
+
+int moe_combine_weighted_bwd(const void *dy, const void *y_perm, const int32_t *slot_to_row,
+                             const float *weights, int dtype, int64_t T, int d, int k,
+                             void *dy_perm, float *d_row_scale, void *stream) {
+  using namespace moe;
+  const char *fn = "moe_combine_weighted_bwd";
+  clear_error();
+  const int rc = check(fn, T, d, k, dtype);
+  if (rc != MOE_OK) return rc;
+  if (T == 0) return MOE_OK;
+  MOE_REQUIRE(dy && slot_to_row && weights && (dy_perm || d_row_scale) && (y_perm || !d_row_scale),
+              MOE_ERR_INVALID_ARG, "%s: null pointer", fn);
+  MOE_REQUIRE(aligned16(dy) && aligned16(y_perm) && aligned16(dy_perm), MOE_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", fn);
+  const int64_t slots = T * k;
+  MOE_REQUIRE(slots < ((int64_t)1 << 26), MOE_ERR_UNSUPPORTED, "%s: too many rows (T=%lld k=%d)",
+              fn, (long long)T, k);   // a launch has below 2^32 threads
+  hipStream_t s = (hipStream_t)stream;
+  const unsigned blocks = (unsigned)((slots + 3) / 4);
+  MOE_LAUNCH("combine_weighted_bwd", s, {
+    if (dtype == MOE_BF16)
+      k_combine_weighted_bwd<bf16_t><<<blocks, 256, 0, s>>>(
+          (const bf16_t *)dy, (const bf16_t *)y_perm, slot_to_row, weights, slots, d, k,
+          (bf16_t *)dy_perm, d_row_scale);
+    else
+      k_combine_weighted_bwd<float><<<blocks, 256, 0, s>>>(
+          (const float *)dy, (const float *)y_perm, slot_to_row, weights, slots, d, k,
+          (float *)dy_perm, d_row_scale);
+  });
+  return check_launch(fn);
+}
+
+}  // extern "C"

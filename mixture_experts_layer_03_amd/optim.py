@@ -1,0 +1,123 @@
+"""AdamW over the tensors of a model, one launch for each 40 of them.
+
+``AdamW`` keeps the states and the step count of a list of parameters and
+issues moe_adamw_step (include/moe.h has the arithmetic):
+
+    opt = AdamW([w_r, w_gu, w_down], lr=1e-4, weight_decay=0.1, state_bits=8, seed=1)
+    blk.backward(...)
+    opt.step([blk.dw_r, blk.dw_gu, blk.dw_down], grad_scale=clip)
+
+States are fp32, or 8 bits with a power of two for each 128 elements.  bf16
+parameters are rounded at random (alike on all ranks that have the same seed),
+unless ``masters`` keeps fp32 copies of them.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import abi
+
+
+def state_shapes(numel: int, state_bits: int):
+    """{name: (elements, dtype)} of one tensor's state."""
+    if state_bits == 32:
+        return {"m": (numel, torch.float32), "v": (numel, torch.float32)}
+    blocks = -(-numel // 128)
+    return {"m": (numel, torch.float8_e4m3fn), "v": (numel, torch.float8_e5m2),
+            "m_scale": (blocks, torch.uint8), "v_scale": (blocks, torch.uint8)}
+
+
+class AdamW:
+    """params: contiguous bf16 or fp32 tensors, all of one type and on one device.
+
+    masters: True for fp32 copies made here, or a list of them; state: a dict
+    of lists of tensors (as ``self.state``) to go on from, with ``step`` its
+    step count.  weight_decay: one number or one for each tensor.  capturable:
+    the step count and the learning rate live on the device, so that a captured
+    step() counts on when it is replayed; ``set_lr`` changes the rate."""
+
+    def __init__(self, params, lr, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01,
+                 state_bits: int = 32, masters=None, seed: int = 0, step: int = 0, state=None,
+                 capturable: bool = False):
+        self.params = list(params)
+        if not self.params:
+            raise ValueError("AdamW: no parameters")
+        if state_bits not in (8, 32):
+            raise ValueError("AdamW: state_bits must be 8 or 32, not %r" % (state_bits,))
+        self.dtype, self.device = self.params[0].dtype, self.params[0].device
+        self.dcode = abi._dtype_code(self.params[0])
+        for i, p in enumerate(self.params):
+            self._need("parameter", i, p, p.numel(), self.dtype)
+        decay = list(weight_decay) if isinstance(weight_decay, (list, tuple)) else [weight_decay] * len(self.params)
+        if len(decay) != len(self.params):
+            raise ValueError("AdamW: %d weight decays for %d parameters" % (len(decay), len(self.params)))
+        self.lr, self.betas, self.eps, self.state_bits = float(lr), betas, eps, state_bits
+        self.seed, self.steps = int(seed) & 0xFFFFFFFFFFFFFFFF, int(step)
+        if masters is True:
+            masters = [p.float() for p in self.params]
+        self.masters = list(masters) if masters else None
+        if self.masters is not None and self.dtype != torch.bfloat16:
+            raise ValueError("AdamW: only bf16 parameters have fp32 copies")
+        names = state_shapes(0, state_bits)
+        if state is None:
+            state = {n: [] for n in names}
+            for p in self.params:
+                for n, (count, dt) in state_shapes(p.numel(), state_bits).items():
+                    t = torch.zeros(count, dtype=dt, device=self.device)
+                    state[n].append(t.fill_(127) if dt == torch.uint8 else t)
+        self.state = {n: list(state[n]) for n in names}
+        for i, p in enumerate(self.params):
+            for n, (count, dt) in state_shapes(p.numel(), state_bits).items():
+                self._need(n, i, self.state[n][i], count, dt)
+            if self.masters is not None:
+                self._need("master", i, self.masters[i], p.numel(), torch.float32)
+        self._table = (abi.AdamwTensor * len(self.params))()
+        for i, p in enumerate(self.params):
+            t = self._table[i]
+            t.param, t.numel, t.weight_decay = p.data_ptr(), p.numel(), float(decay[i])
+            t.m, t.v = self.state["m"][i].data_ptr(), self.state["v"][i].data_ptr()
+            if state_bits == 8:
+                t.m_scale, t.v_scale = self.state["m_scale"][i].data_ptr(), self.state["v_scale"][i].data_ptr()
+            if self.masters is not None:
+                t.master = self.masters[i].data_ptr()
+        self.lr_dev = self.step_dev = None
+        if capturable:
+            self.lr_dev = torch.full((1,), self.lr, dtype=torch.float32, device=self.device)
+            self.step_dev = torch.full((1,), self.steps, dtype=torch.int64, device=self.device)
+
+    def _need(self, what, i, t, numel, dtype):
+        if t.numel() != numel or t.dtype != dtype or t.device != self.device or not t.is_contiguous():
+            raise ValueError("AdamW: %s %d must be contiguous, %d of %s on %s, not %s of %s on %s"
+                             % (what, i, numel, dtype, self.device, tuple(t.shape), t.dtype, t.device))
+
+    def set_lr(self, lr: float):
+        self.lr = float(lr)
+        if self.lr_dev is not None:
+            self.lr_dev.fill_(self.lr)
+
+    def step(self, grads, grad_scale=None, stream=None):
+        """One step in place.  grads: a tensor for each parameter, all fp32 or (bf16 parameters)
+        all bf16; grad_scale: an fp32 device tensor of one element that multiplies them, or None.
+        Everything runs on `stream` (the current one); with capturable that has to be the current
+        one, since the count is stepped there (``step_dev``; ``steps`` counts calls, not replays)."""
+        if len(grads) != len(self.params):
+            raise ValueError("AdamW: %d gradients for %d parameters" % (len(grads), len(self.params)))
+        table, dtype, device = self._table, grads[0].dtype, self.device
+        gcode = abi._dtype_code(grads[0])
+        for i, (g, p) in enumerate(zip(grads, self.params)):
+            if g.dtype != dtype or g.shape != p.shape or not g.is_contiguous() or g.device != device:
+                self._need("gradient", i, g, p.numel(), dtype)
+            t = table[i]
+            t.grad = g.data_ptr()
+            if (t.param or 0) != p.data_ptr():
+                raise ValueError("AdamW: parameter %d has moved" % i)
+        if grad_scale is not None:
+            self._need("grad_scale", 0, grad_scale, 1, torch.float32)
+        if device.type != "cuda" or device.index != torch.cuda.current_device():
+            raise ValueError("AdamW: the parameters are on %s, not on the current device" % device)
+        if self.step_dev is not None:
+            self.step_dev.add_(1)
+        abi.moe_adamw_step(table, len(self.params), self.dcode, gcode, self.state_bits,
+                           self.lr, self.betas[0], self.betas[1], self.eps, self.steps + 1, self.seed,
+                           grad_scale, self.lr_dev, self.step_dev, stream)
+        self.steps += 1

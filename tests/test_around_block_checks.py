@@ -1,0 +1,219 @@
+"""What the residual norms, the weighted combine and AdamW refuse, on the host before any launch (no GPU needed)."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from mixture_experts_layer_03_amd import abi
+from mixture_experts_layer_03_amd.optim import AdamW, state_shapes
+from oracle import around_block as O
+
+P = ctypes.c_void_p(0x1000)      # never dereferenced
+ODD = ctypes.c_void_p(0x1008)
+N = None
+
+
+def _norm(x=P, y=P, gate=N, kind=0, wp=P, wn=P, scale=1.0, eps=1e-6, dtype=1, T=4, d=64, out=P, n=P, rp=P, rn=P):
+    return abi.lib().moe_residual_norm(x, y, gate, kind, wp, wn, scale, eps, dtype, T, d, out, n, rp, rn, N)
+
+
+def _bwd(d_out=P, d_n=P, out=P, y=P, gate=N, kind=0, wp=P, wn=P, rp=P, rn=P, dtype=1, T=4, d=64, d_x=P, d_y=P, dwp=P, dwn=P,
+         dg=N, ws=P, size=1 << 20):
+    return abi.lib().moe_residual_norm_bwd(d_out, d_n, out, y, gate, kind, wp, wn, rp, rn, 1.0, dtype, T, d, d_x, d_y, dwp,
+                                           dwn, dg, ws, size, N)
+
+
+def _combine(y_perm=P, rows=P, w=P, k=2, x=P, gate=N, kind=0, T=4, d=64, out=P, n=P):
+    return abi.lib().moe_combine_residual_norm(y_perm, rows, w, k, x, gate, kind, P, P, 1.0, 1e-6, 1, T, d, N, out, n, P, P, N)
+
+
+@pytest.mark.parametrize("rc,kw", [
+    (-1, dict(T=-1)), (-1, dict(d=0)), (-2, dict(d=12)), (-2, dict(d=16392)), (-2, dict(dtype=2)), (-2, dict(T=1 << 26)),
+    (-1, dict(kind=4, gate=P)), (-1, dict(kind=1)), (-1, dict(gate=P)), (-1, dict(eps=0.0)), (-1, dict(eps=float("nan"))),
+    (-1, dict(n=N)), (-1, dict(wn=N)), (-1, dict(wp=N)), (-1, dict(out=N)), (-1, dict(x=ODD)), (-1, dict(n=ODD)),
+    (-1, dict(y=N)), (-1, dict(y=N, out=N, wp=N, rp=N, scale=0.5)), (-1, dict(y=N, out=N, wp=N, rp=N, x=N)),
+    (-1, dict(wn=N, n=N)),       # rstd_pre without its norm
+])
+def test_residual_norm(rc, kw):
+    assert _norm(**kw) == rc
+    assert abi.lib().moe_last_error()
+
+
+@pytest.mark.parametrize("rc,kw", [
+    (-1, dict(T=-1)), (-2, dict(d=20)), (-2, dict(dtype=9)), (-1, dict(d_out=N, d_n=N, wn=N, dwn=N)), (-1, dict(d_n=N)),
+    (-1, dict(wn=N)), (-1, dict(rn=N)), (-1, dict(rp=N)), (-1, dict(out=N)), (-1, dict(y=N)), (-1, dict(dg=P)),
+    (-1, dict(wp=N)), (-1, dict(kind=1)), (-1, dict(d_y=ODD)), (-3, dict(ws=N)), (-3, dict(size=100)),
+    (-1, dict(d_x=N, d_y=N, dwp=N, dwn=N)), (-1, dict(wp=N, rp=N, dwp=N, y=N, kind=1, gate=P, dg=P)),
+])
+def test_residual_norm_bwd(rc, kw):
+    assert _bwd(**kw) == rc
+
+
+@pytest.mark.parametrize("rc,kw", [
+    (-1, dict(y_perm=N)), (-1, dict(rows=N)), (-1, dict(k=0)), (-1, dict(k=33)), (-1, dict(out=N)), (-2, dict(d=4)),
+    (-1, dict(n=N)), (-2, dict(T=1 << 30)),
+])
+def test_combine_residual_norm(rc, kw):
+    assert _combine(**kw) == rc
+
+
+def test_weighted_combine():
+    f, b = abi.lib().moe_combine_weighted, abi.lib().moe_combine_weighted_bwd
+    assert f(P, P, P, 1, -1, 64, 2, P, N) == -1
+    assert f(P, P, P, 1, 4, 63, 2, P, N) == -2
+    assert f(P, P, P, 3, 4, 64, 2, P, N) == -2
+    assert f(P, P, P, 1, 4, 64, 33, P, N) == -2
+    assert f(P, P, N, 1, 4, 64, 2, P, N) == -1
+    assert f(ODD, P, P, 1, 4, 64, 2, P, N) == -1
+    assert f(P, P, P, 1, 1 << 30, 64, 2, P, N) == -2
+    assert f(P, P, P, 1, 1 << 29, 64, 2, P, N) == -2
+    assert f(N, N, N, 1, 0, 64, 2, N, N) == 0
+    assert b(P, P, P, P, 1, 4, 64, 2, N, N, N) == -1
+    assert b(P, N, P, P, 1, 4, 64, 2, P, P, N) == -1
+    assert b(P, P, P, P, 1, 1 << 26, 64, 2, P, P, N) == -2
+    assert b(P, P, P, P, 1, 4, 64, 2, ODD, P, N) == -1
+
+
+def _adamw(change=None, n=2, pd=1, gd=0, bits=8, lr=1e-3, b1=0.9, b2=0.999, eps=1e-8, step=1, lr_dev=N, step_dev=N, tensors=True):
+    t = (abi.AdamwTensor * 2)()
+    for i in range(2):
+        for name in ("param", "grad", "m", "v", "m_scale", "v_scale"):
+            setattr(t[i], name, 0x1000 * (1 + i) + 0x100000 * len(name))
+        t[i].numel = 64
+    if change:
+        change(t)
+    return abi.lib().moe_adamw_step(ctypes.addressof(t) if tensors else N, n, pd, gd, bits, lr, b1, b2, eps, step, 1, N, lr_dev,
+                                    step_dev, N)
+
+
+def _set(**kw):
+    return lambda t: [setattr(t[1], k, v) for k, v in kw.items()]
+
+
+@pytest.mark.parametrize("rc,kw", [
+    (-1, dict(n=-1)), (-1, dict(tensors=False)), (-2, dict(pd=3)), (-2, dict(pd=0, gd=1)), (-2, dict(bits=16)), (-1, dict(b1=1.0)),
+    (-1, dict(b2=-0.1)), (-1, dict(eps=0.0)), (-1, dict(eps=float("inf"))), (-1, dict(step=0)), (-1, dict(step=1 << 32)),
+    (-1, dict(lr=float("nan"))), (-1, dict(lr_dev=P)), (-1, dict(step_dev=P)),
+    (-1, dict(change=_set(param=None))), (-1, dict(change=_set(grad=None))), (-1, dict(change=_set(m_scale=None))),
+    (-1, dict(change=_set(m=0x1008))), (-1, dict(change=_set(master=0x7000))), (-2, dict(change=_set(numel=-1))),
+    (-2, dict(change=_set(numel=1 << 40))), (-1, dict(change=_set(weight_decay=float("inf")))),
+    (-1, dict(change=lambda t: setattr(t[1], "param", t[0].param))), (-1, dict(change=lambda t: setattr(t[1], "v", t[0].v))),
+])
+def test_adamw(rc, kw):
+    assert _adamw(**kw) == rc
+    assert abi.lib().moe_last_error()
+
+
+def test_adamw_fp32_parameters_have_no_copy():
+    def both(t):
+        t[0].master, t[1].master = 0x7000, 0x8000
+    assert _adamw(both, pd=0) == -1
+
+
+def test_adamw_without_elements():
+    def empty(t):
+        for i in range(2):
+            t[i].numel, t[i].param = 0, None
+    assert _adamw(empty) == 0
+    assert _adamw(n=0) == 0
+
+
+def test_optimizer_arguments():
+    z = lambda *s, dt=torch.float32: torch.zeros(*s, dtype=dt)
+    with pytest.raises(ValueError):
+        AdamW([], lr=1e-3)
+    with pytest.raises(ValueError):
+        AdamW([z(4)], lr=1e-3, state_bits=4)
+    with pytest.raises(ValueError):
+        AdamW([z(4), z(4, dt=torch.bfloat16)], lr=1e-3)
+    with pytest.raises(ValueError):
+        AdamW([z(4, 4).t()[:2]], lr=1e-3)
+    with pytest.raises(ValueError):
+        AdamW([z(4)], lr=1e-3, masters=True)
+    with pytest.raises(ValueError):
+        AdamW([z(4)], lr=1e-3, weight_decay=[0.1, 0.2])
+    with pytest.raises(ValueError):
+        AdamW([z(4)], lr=1e-3, state={"m": [z(3)], "v": [z(4)]})
+    with pytest.raises(TypeError):
+        AdamW([z(4, dt=torch.float64)], lr=1e-3)
+    opt = AdamW([z(300)], lr=1e-3, state_bits=8)
+    assert opt.state["m_scale"][0].shape == (3,) and (opt.state["m_scale"][0] == 127).all()
+    with pytest.raises(ValueError):
+        opt.step([])
+    with pytest.raises(ValueError):
+        opt.step([z(299)])
+    with pytest.raises(TypeError):
+        opt.step([z(300).double()])
+    with pytest.raises(ValueError):
+        opt.step([z(300)])           # not on a GPU
+
+
+def test_tensors_of_another_shape_type_or_stride():
+    z = lambda *s, dt=torch.bfloat16: torch.zeros(*s, dtype=dt)
+    x, w = z(4, 64), z(64)
+    for bad in (dict(out=z(4, 72)), dict(n=z(4, 64, dt=torch.float32)), dict(w_post=z(64, dt=torch.float32)), dict(gate=z(4)),
+                dict(gate=z(4, 1)), dict(y=z(64, 4).t()), dict(rstd_pre=z(4))):
+        kw = dict(x=x, y=z(4, 64), out=z(4, 64), n=z(4, 64), w_post=w, w_pre=w)
+        kw.update(bad)
+        with pytest.raises(ValueError):
+            abi.moe_residual_norm(**kw)
+    f32 = lambda *s: z(*s, dt=torch.float32)
+    rows = torch.zeros(8, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        abi.moe_combine_weighted(z(8, 64), rows.long(), f32(4, 2), x)
+    with pytest.raises(ValueError):
+        abi.moe_combine_weighted(z(8, 72), rows, f32(4, 2), x)
+    with pytest.raises(ValueError):
+        abi.moe_combine_weighted_bwd(x, z(8, 64), rows, f32(4, 2), z(7, 64), f32(8))
+    with pytest.raises(ValueError):
+        abi.moe_combine_residual_norm(z(8, 64), rows[:7], f32(4, 2), 2, x, x, x)
+
+
+# ---------------------------------------------------------------- the oracle itself
+
+def test_8_bit_values_and_rounding():
+    for fmt, dt in (("e4m3", torch.float8_e4m3fn), ("e5m2", torch.float8_e5m2)):
+        v = O.grid(fmt)
+        codes = torch.arange(len(v), dtype=torch.uint8)
+        assert np.array_equal(codes.view(dt).double().numpy(), v)
+        # every value stays itself whatever the random bits, with any power of two
+        for s in (-126, 0, 60):
+            for r in (0, 0xFFFF):
+                r16 = np.full(len(v), r)
+                got = O.code_of(v * 2.0 ** s, np.full(1, s), r16, fmt)
+                assert np.array_equal(got, codes.numpy())
+        # a quarter of the way up: the upper one for a quarter of the random bits
+        x = v[20] + 0.25 * (v[21] - v[20])
+        r16 = np.arange(1 << 16)
+        got = O.code_of(np.full(1 << 16, x), np.zeros(1 << 9, int), r16, fmt)
+        assert (got == 21).sum() == 1 << 14 and (got == 20).sum() == 3 << 14
+
+
+def test_moments_and_bf16_rounding():
+    p = np.float32([1.0, -1.0, 1.0 + 2.0 ** -9, 0.0, np.inf])
+    assert np.array_equal(O.bf16_up_or_down(p, np.uint64(0xFFFF)), np.float32([1.0, -1.0, 1.0 + 2.0 ** -7, 0.0, np.inf]))
+    assert np.array_equal(O.bf16_up_or_down(p, np.uint64(0)), np.float32([1.0, -1.0, 1.0, 0.0, np.inf]))
+    assert [int(x) for x in O.exponents(np.float32([448.0] + [0.0] * 127 + [449.0]), 448.0)] == [0, 1]
+    assert int(O.exponents(np.array([1e-42], np.float32), 448.0)[0]) == -126
+
+
+def test_norm_gradients_of_the_oracle_against_autograd():
+    g = torch.Generator().manual_seed(2)
+    T, d = 5, 16
+    mk = lambda *s: torch.randn(*s, generator=g, dtype=torch.float64, requires_grad=True)
+    x, y, wp, wn = mk(T, d), mk(T, d), mk(d), mk(d)
+    for gate in (None, mk(d), mk(T, 1), mk(T, d)):
+        norm = lambda v, w: v * (v.square().mean(1, keepdim=True) + 1e-5).rsqrt() * w
+        p = norm(y, wp)
+        out = 0.5 * x + (p if gate is None else p * gate)
+        n = norm(out, wn)
+        go, gn = torch.randn(T, d, generator=g).double(), torch.randn(T, d, generator=g).double()
+        leaves = [x, y, wp, wn] + ([] if gate is None else [gate])
+        grads = torch.autograd.grad((out * go).sum() + (n * gn).sum(), leaves)
+        num = lambda t: None if t is None else t.detach().numpy()
+        o, _, rp, rn, _ = O.residual_norm(num(x), num(y), num(wp), num(wn), num(gate), 0.5, 1e-5, lambda v: v)
+        assert np.allclose(o, num(out), rtol=1e-12)
+        r = O.residual_norm_bwd(go.numpy(), gn.numpy(), o, num(y), num(wp), num(wn), num(gate), 0.5, rp, rn)
+        for name, t in zip(("d_x", "d_y", "d_w_post", "d_w_pre", "d_gate"), grads):
+            assert np.allclose(r[name][0].reshape(t.shape), num(t), rtol=1e-9, atol=1e-11), name
