@@ -11,7 +11,7 @@
 namespace moe {
 namespace {
 
-// One wave for 128 16-byte pieces of a token's row, four expert rows in flight.
+// One wave for kPieces x 64 16-byte pieces of a token's row, four expert rows in flight.
 constexpr int kPieces = 2;
 template <typename T>
 __global__ __launch_bounds__(256) void k_combine_weighted(const T *__restrict__ y_perm,
@@ -24,28 +24,26 @@ __global__ __launch_bounds__(256) void k_combine_weighted(const T *__restrict__ 
   const int64_t t = wid / parts;
   if (t >= ntok) return;
   const int lane = threadIdx.x & 63;
-  const int c0 = (int)(wid - t * parts) * 64 * kPieces + lane;
+  const uint32_t c0 = (uint32_t)((int)(wid - t * parts) * 64 * kPieces + lane) * 16u;
+  const uint32_t bytes = (uint32_t)d * sizeof(T);
   const int myr = lane < k ? slot_to_row[t * k + lane] : -1;   // k <= 32
-  const float myw = lane < k ? w[t * k + lane] : 0.0f;
-  const u32x4_t zero = {0u, 0u, 0u, 0u};
+  const float myw = myr < 0 ? 0.0f : w[t * k + lane];
   float acc[kPieces][N];
 #pragma unroll
   for (int h = 0; h < kPieces; ++h)
 #pragma unroll
     for (int i = 0; i < N; ++i) acc[h][i] = 0.0f;
-  for (int j = 0; j < k; j += 4) {
+  for (int j = 0; j < k; j += 4) {   // a row that is not there adds 0 * 0
     u32x4_t v[4][kPieces];
-    int r[4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      r[u] = j + u < k ? __builtin_amdgcn_readlane(myr, j + u) : -1;
-      const u32x4_t *row = reinterpret_cast<const u32x4_t *>(y_perm + (int64_t)max(r[u], 0) * d);
+    for (int u = 0; u < 4; ++u) {   // lanes from k on hold -1 (j + u <= 34)
+      const int r = __builtin_amdgcn_readlane(myr, j + u);
+      const Row row(y_perm, (int64_t)r * bytes, r >= 0, bytes);
 #pragma unroll
-      for (int h = 0; h < kPieces; ++h) v[u][h] = r[u] >= 0 && c0 + 64 * h < nvec ? row[c0 + 64 * h] : zero;
+      for (int h = 0; h < kPieces; ++h) v[u][h] = row.load(c0 + 1024u * h);
     }
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      if (r[u] < 0) continue;
       const float wj = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(myw), j + u));
 #pragma unroll
       for (int h = 0; h < kPieces; ++h) {
@@ -56,22 +54,20 @@ __global__ __launch_bounds__(256) void k_combine_weighted(const T *__restrict__ 
       }
     }
   }
-  u32x4_t *o = reinterpret_cast<u32x4_t *>(y + t * d);
+  const Row to(y, t * bytes, true, bytes);
 #pragma unroll
-  for (int h = 0; h < kPieces; ++h)
-    if (c0 + 64 * h < nvec) o[c0 + 64 * h] = pack(acc[h], (const T *)nullptr);
+  for (int h = 0; h < kPieces; ++h) to.store(c0 + 1024u * h, pack(acc[h], (const T *)nullptr));
 }
 
 // One wave for each slot; the waves of a token's slots lie next to each other,
 // so that its row of dy comes from HBM once.
-constexpr int kSteps = 3;   // 16-byte pieces of a row that a lane has in flight
+constexpr int kSteps = 6;   // 16-byte pieces of a row that a lane has in flight
 template <typename T>
 __global__ __launch_bounds__(256) void k_combine_weighted_bwd(
     const T *__restrict__ dy, const T *__restrict__ y_perm, const int32_t *__restrict__ slot_to_row,
     const float *__restrict__ w, int64_t nslot, int d, int k, T *__restrict__ dy_perm,
     float *__restrict__ d_row_scale) {
   constexpr int N = kVec<T>;
-  const int nvec = d / N;
   const int64_t slot = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   if (slot >= nslot) return;
   const int r = slot_to_row[slot];
@@ -79,18 +75,16 @@ __global__ __launch_bounds__(256) void k_combine_weighted_bwd(
   const float wj = w[slot];
   const int lane = threadIdx.x & 63;
   const int64_t t = (int64_t)((uint32_t)slot / (uint32_t)k);   // slots are below 2^31
-  const u32x4_t *g = reinterpret_cast<const u32x4_t *>(dy + t * d);
-  const u32x4_t *yr = reinterpret_cast<const u32x4_t *>(y_perm + (int64_t)r * d);
-  u32x4_t *o = reinterpret_cast<u32x4_t *>(dy_perm + (int64_t)r * d);
-  const u32x4_t zero = {0u, 0u, 0u, 0u};
+  const uint32_t bytes = (uint32_t)d * sizeof(T);
+  const Row g(dy, t * bytes, true, bytes), yr(y_perm, (int64_t)r * bytes, d_row_scale, bytes);
+  const Row to(dy_perm, (int64_t)r * bytes, dy_perm, bytes);
   float dot = 0.0f;
-  for (int c = lane; c < nvec; c += 64 * kSteps) {
+  for (uint32_t c = lane * 16u; c < bytes; c += 1024u * kSteps) {
     u32x4_t a[kSteps], b[kSteps];
 #pragma unroll
     for (int h = 0; h < kSteps; ++h) {
-      const bool ok = c + 64 * h < nvec;
-      a[h] = ok ? g[c + 64 * h] : zero;
-      b[h] = ok && d_row_scale ? yr[c + 64 * h] : zero;
+      a[h] = g.keep(c + 1024u * h);
+      b[h] = yr.load(c + 1024u * h);
     }
 #pragma unroll
     for (int h = 0; h < kSteps; ++h) {
@@ -102,7 +96,7 @@ __global__ __launch_bounds__(256) void k_combine_weighted_bwd(
         dot = fmaf(f[i], q[i], dot);
         f[i] *= wj;
       }
-      if (dy_perm && c + 64 * h < nvec) o[c + 64 * h] = pack(f, (const T *)nullptr);
+      to.store(c + 1024u * h, pack(f, (const T *)nullptr));
     }
   }
   if (!d_row_scale) return;

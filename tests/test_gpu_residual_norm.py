@@ -7,7 +7,7 @@ products bring p to 52 v of itself.  The three sums of the backward have the
 same shape, up to 100 v of the sum of their addends' absolute values, with up
 to 8 roundings in an addend; c1, c2 and the last combination stay below 16
 more: 128 v of everything that is added.  Sums over the tokens: at most
-T / 768 + 1 rows in a lane, 48 blocks in a wave and 16 waves.
+T / 256 + 1 rows in a lane, 192 blocks in a wave and 16 waves.
 """
 import numpy as np
 import pytest
@@ -53,7 +53,7 @@ def _close(name, got, ref, tol):
 
 
 # d: one piece, a part of a wave, several waves, past 512, 1024 and 2048 pieces, the largest
-SHAPES = [(1, 8), (3, 64), (5, 520), (7, 2880), (2, 4104), (3, 8200), (2, 16384), (2051, 1032), (2049, 2880), (2050, 4096)]
+SHAPES = [(1, 8), (2055, 72), (2500, 776), (2049, 1544), (2048, 2056), (3, 64), (5, 520), (7, 2880), (2, 4104), (3, 8200), (2, 16384), (2051, 1032), (2049, 2880), (2050, 4096)]
 
 
 def _check_forward(x, y, out, n, rp, rn, wp, wn, gt, scale, eps):
@@ -106,7 +106,7 @@ def test_backward(T, d, dtype, post, pre, gate):
     ref = O.residual_norm_bwd(_np(d_out), _np(d_n), _np(o), _np(y), _np(wp), _np(wn), _np(gt), 0.75, col(rp), col(rn))
     got = {"d_x": d_x, "d_y": d_y, "d_w_post": dwp, "d_w_pre": dwn, "d_gate": dg}
     assert {n for n, t in got.items() if t is not None} == set(ref)
-    over_t = T / 768 + 1 + 48 + 16
+    over_t = T / 256 + 1 + 3072 / 16 + 16
     for name, (v, size) in ref.items():
         t = got[name]
         sums = over_t if name.startswith("d_w") or (name == "d_gate" and gate == "channel") else 0
