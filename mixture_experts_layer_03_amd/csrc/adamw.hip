@@ -17,6 +17,7 @@
 #include <algorithm>
 #include <cmath>
 #include <functional>
+#include <type_traits>
 #include <vector>
 
 #include "rows.h"
@@ -59,9 +60,8 @@ __device__ __forceinline__ uint32_t mix(uint32_t a) {
 }
 
 // The largest of 16 neighbouring lanes' values, in all of them.
-__device__ __forceinline__ float max16(float v) {
-#define MOE_ROR(n) \
-  v = fmaxf(v, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x120 + n, 0xf, 0xf, true)))
+__device__ __forceinline__ uint32_t max16(uint32_t v) {
+#define MOE_ROR(n) v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x120 + n, 0xf, 0xf, true))
   MOE_ROR(8);
   MOE_ROR(4);
   MOE_ROR(2);
@@ -70,28 +70,14 @@ __device__ __forceinline__ float max16(float v) {
   return v;
 }
 
-__device__ __forceinline__ bool finite(float v) { return (__float_as_uint(v) & 0x7f800000u) != 0x7f800000u; }
+constexpr uint32_t kInf = 0x7f800000u;
+__device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
 // The smallest s >= -126 with amax <= 1.75 * 2^top * 2^s; 0 for an empty block.
 template <int TOP>
-__device__ __forceinline__ int block_exponent(float amax) {
-  const uint32_t b = __float_as_uint(amax);
-  const int s = (int)(b >> 23) - 127 - TOP + ((b & 0x7fffffu) > 0x600000u);
-  return b == 0 ? 0 : max(s, -126);
-}
-
-// |x| times the block's inverse scale, at most 1.75 * 2^(its largest exponent),
-// to 8 bits: MANT mantissa bits, exponent bias BIAS, 16 random bits below the
-// last.  The scaling is exact but for values that are far below the smallest
-// code.  No carry leaves the format: the largest value has no bits below its last.
-template <int MANT, int BIAS>
-__device__ __forceinline__ uint32_t to8(float a, uint32_t r16) {
-  constexpr int cut = 23 - MANT;
-  constexpr float least = 1.0f / (float)(1 << (BIAS - 1));            // smallest normal
-  const uint32_t r = r16 << (cut - 16);
-  const uint32_t normal = ((__float_as_uint(a) + r) >> cut) - (uint32_t)((127 - BIAS) << MANT);
-  const uint32_t low = ((uint32_t)(fminf(a, least) * __uint_as_float((uint32_t)(127 + BIAS - 1 + MANT + cut) << 23)) + r) >> cut;
-  return a >= least ? normal : low;
+__device__ __forceinline__ int block_exponent(uint32_t amax) {
+  const int s = (int)(amax >> 23) - 127 - TOP + ((amax & 0x7fffffu) > 0x600000u);
+  return amax == 0 ? 0 : max(s, -126);
 }
 
 template <typename T, int V>
@@ -100,13 +86,13 @@ __device__ __forceinline__ void load_row(const void *base, int64_t i, int64_t n,
     if constexpr (sizeof(T) == 4) {
 #pragma unroll
       for (int q = 0; q < V / 4; ++q) {
-        const u32x4_t v = *reinterpret_cast<const u32x4_t *>((const float *)base + i + 4 * q);
+        const u32x4_t v = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t *>((const float *)base + i + 4 * q));
 #pragma unroll
         for (int e = 0; e < 4; ++e) f[4 * q + e] = __uint_as_float(v[e]);
       }
     } else {
-      uint32_t w[V / 2];
-      __builtin_memcpy(w, __builtin_assume_aligned((const bf16_t *)base + i, 2 * V), 2 * V);
+      typedef uint32_t words __attribute__((ext_vector_type(V / 2)));
+      const words w = __builtin_nontemporal_load(reinterpret_cast<const words *>((const bf16_t *)base + i));
 #pragma unroll
       for (int e = 0; e < V / 2; ++e) {
         f[2 * e] = bf16_bits_to_f32(w[e] & 0xffffu);
@@ -119,6 +105,30 @@ __device__ __forceinline__ void load_row(const void *base, int64_t i, int64_t n,
   for (int e = 0; e < V; ++e) f[e] = i + e < n ? Store<T>::load((const T *)base + i + e) : 0.0f;
 }
 
+// V elements as words (two bf16 in one)
+template <typename T, int V>
+__device__ __forceinline__ void store_words(void *base, int64_t i, int64_t n,
+                                            const uint32_t (&w)[V * sizeof(T) / 4]) {
+  constexpr int kWords = V * (int)sizeof(T) / 4, kEach = kWords < 4 ? kWords : 4;
+  typedef uint32_t words __attribute__((ext_vector_type(kEach)));
+  T *p = (T *)base + i;
+  if (i + V <= n) {
+#pragma unroll
+    for (int q = 0; q < kWords; q += kEach) {
+      words x;
+#pragma unroll
+      for (int e = 0; e < kEach; ++e) x[e] = w[q + e];
+      __builtin_nontemporal_store(x, reinterpret_cast<words *>(p) + q / kEach);
+    }
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    if (i + e >= n) continue;
+    if constexpr (sizeof(T) == 4) p[e] = __uint_as_float(w[e]);
+    else p[e] = (bf16_t)(w[e / 2] >> (16 * (e & 1)));
+  }
+}
 template <typename T, int V>
 __device__ __forceinline__ void store_row(void *base, int64_t i, int64_t n, const float (&f)[V]) {
   uint32_t w[V * sizeof(T) / 4];
@@ -127,22 +137,12 @@ __device__ __forceinline__ void store_row(void *base, int64_t i, int64_t n, cons
     if constexpr (sizeof(T) == 4) w[e] = __float_as_uint(f[e]);
     else w[e / 2] = pack_bf16x2(f[e], f[e + 1]);
   }
-  T *p = (T *)base + i;
-  if (i + V <= n) {
-    __builtin_memcpy(__builtin_assume_aligned(p, sizeof(T) * V < 16 ? sizeof(T) * V : 16), w, sizeof(T) * V);
-    return;
-  }
-#pragma unroll
-  for (int e = 0; e < V; ++e) {
-    if (i + e >= n) continue;
-    if constexpr (sizeof(T) == 4) p[e] = f[e];
-    else p[e] = (bf16_t)(w[e / 2] >> (16 * (e & 1)));
-  }
+  store_words<T, V>(base, i, n, w);
 }
 
 __device__ __forceinline__ u32x2_t load8(const void *base, int64_t i, int64_t n) {
   const uint8_t *p = (const uint8_t *)base + i;
-  if (i + 8 <= n) return *reinterpret_cast<const u32x2_t *>(p);
+  if (i + 8 <= n) return __builtin_nontemporal_load(reinterpret_cast<const u32x2_t *>(p));
   u32x2_t w = {0u, 0u};
 #pragma unroll
   for (int e = 0; e < 8; ++e)
@@ -152,7 +152,7 @@ __device__ __forceinline__ u32x2_t load8(const void *base, int64_t i, int64_t n)
 __device__ __forceinline__ void store8(void *base, int64_t i, int64_t n, u32x2_t w) {
   uint8_t *p = (uint8_t *)base + i;
   if (i + 8 <= n) {
-    *reinterpret_cast<u32x2_t *>(p) = w;
+    __builtin_nontemporal_store(w, reinterpret_cast<u32x2_t *>(p));
     return;
   }
 #pragma unroll
@@ -162,8 +162,12 @@ __device__ __forceinline__ void store8(void *base, int64_t i, int64_t n, u32x2_t
 
 // P, G: types of parameter and gradient.  A thread takes V neighbouring
 // elements, a block 256 V of them; 16 lanes share the scale of 128 (i >> 7).
+// Five waves a SIMD with 32-bit states: more of them have more lines under way
+// than HBM serves in order (30 bytes an element: 6.3 TB/s with 5, 6.1 with 8 or
+// 4); 8-bit states need the sixth for their arithmetic.
 template <typename P, typename G, bool MASTER, bool EIGHT>
-__global__ __launch_bounds__(256) void k_adamw(const AdamArgs a) {
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(EIGHT ? 6 : 5, EIGHT ? 6 : 5))) void k_adamw(
+    const AdamArgs a) {
 #pragma clang fp contract(off)
   constexpr int V = EIGHT ? 8 : 4;
   constexpr bool RANDOM_P = sizeof(P) == 2 && !MASTER;
@@ -221,40 +225,71 @@ __global__ __launch_bounds__(256) void k_adamw(const AdamArgs a) {
     v[e] = v[e] * a.b2 + ge * a.a2 * ge;
     // 1-ulp root and reciprocal: off by 2^-22 of the update, below the
     // rounding of p wherever the update is below p/4
-    const float den = __builtin_amdgcn_sqrtf(v[e]) * rbc2 + a.eps;
-    p[e] = p[e] * decay - step_size * (m[e] * __builtin_amdgcn_rcpf(den));
+    const float den = fmaf(__builtin_amdgcn_sqrtf(v[e]), rbc2, a.eps);
+    p[e] = fmaf(-step_size, m[e] * __builtin_amdgcn_rcpf(den), p[e] * decay);
   }
 
+  // The conversions below round a magnitude up where the bits that it loses
+  // and the top bits of the random operand carry (measured: as bit arithmetic
+  // on the fp32 pattern does, denormal results included; infinities and NaN stay).
   uint32_t r[V];
   if constexpr (RANDOM_P || EIGHT) {
     const uint32_t key =
-        mix(mix(mix(mix(a.seed_lo) ^ a.seed_hi) ^ step) ^ t.index) ^ (uint32_t)(i >> 32);
+        mix(mix(mix(mix(a.seed_lo) ^ a.seed_hi) ^ step) ^ t.index) ^ (uint32_t)(i >> 32) ^ (uint32_t)i;
 #pragma unroll
-    for (int e = 0; e < V; ++e) r[e] = mix(key ^ ((uint32_t)i + e));
+    for (int e = 0; e < V; ++e) r[e] = mix(key ^ e);   // i is a multiple of V
   }
   if constexpr (EIGHT) {
-    float m_max = 0.0f, v_max = 0.0f;
+    uint32_t m_max = 0, v_max = 0;
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-      m_max = finite(m[e]) ? fmaxf(m_max, fabsf(m[e])) : m_max;
-      v_max = finite(v[e]) ? fmaxf(v_max, fabsf(v[e])) : v_max;
+      m_max = max(m_max, magnitude(m[e]));
+      v_max = max(v_max, magnitude(v[e]));
     }
-    const int ms = block_exponent<8>(max16(m_max)), vs = block_exponent<15>(max16(v_max));
+    m_max = max16(m_max), v_max = max16(v_max);
+    const bool bad = __any(max(m_max, v_max) >= kInf);   // somewhere in the wave
+    if (bad) {   // only what is finite scales a block
+      m_max = v_max = 0;
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        uint32_t mm = magnitude(m[e]), vm = magnitude(v[e]);
+        asm volatile("" : "+v"(mm), "+v"(vm));   // keeps the branch: no selects for every block
+        m_max = max(m_max, mm < kInf ? mm : 0u);
+        v_max = max(v_max, vm < kInf ? vm : 0u);
+      }
+      m_max = max16(m_max), v_max = max16(v_max);
+    }
+    const int ms = block_exponent<8>(m_max), vs = block_exponent<15>(v_max);
     const float mi = __uint_as_float((uint32_t)(127 - ms) << 23), vi = __uint_as_float((uint32_t)(127 - vs) << 23);
-    u32x2_t mq = {0u, 0u}, vq = {0u, 0u};
+    uint32_t mq[2] = {0u, 0u}, vq[2] = {0u, 0u};
+    auto code = [&](int e, auto sel) {
+      const float am = m[e] * mi;
+      // a second moment that is not zero never becomes it, since its root
+      // divides: at least the smallest code, 2^-16
+      const float av = v[e] > 0.0f ? fmaxf(v[e] * vi, 0x1p-16f) : v[e] * vi;
+      mq[e / 4] = (uint32_t)__builtin_amdgcn_cvt_sr_fp8_f32(am, r[e] & 0xffff0000u, (int)mq[e / 4], decltype(sel)::value);
+      vq[e / 4] = (uint32_t)__builtin_amdgcn_cvt_sr_bf8_f32(av, (r[e] * 0x30e9132du) & 0xffff0000u, (int)vq[e / 4],
+                                                            decltype(sel)::value);
+    };
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      uint32_t cm = to8<3, 7>(fabsf(m[e]) * mi, r[e] >> 16) | ((__float_as_uint(m[e]) >> 24) & 0x80u);
-      uint32_t cv = to8<2, 15>(fabsf(v[e]) * vi, (r[e] * 0x30e9132du) >> 16);
-      // a second moment that is not zero never becomes it: its root divides
-      if (v[e] > 0.0f) cv = max(cv, 1u);
-      if (!finite(m[e])) cm = 0x7fu;
-      if (!finite(v[e])) cv = 0x7fu;
-      mq[e / 4] |= cm << (8 * (e & 3));
-      vq[e / 4] |= cv << (8 * (e & 3));
+    for (int e = 0; e < V; e += 4) {
+      code(e, std::integral_constant<int, 0>());
+      code(e + 1, std::integral_constant<int, 1>());
+      code(e + 2, std::integral_constant<int, 2>());
+      code(e + 3, std::integral_constant<int, 3>());
     }
-    store8(t.m, i, n, mq);
-    store8(t.v, i, n, vq);
+    if (bad) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const uint32_t at = 0xffu << (8 * (e & 3)), nan = 0x7fu << (8 * (e & 3));
+        uint32_t mm = magnitude(m[e]), vm = magnitude(v[e]);
+        asm volatile("" : "+v"(mm), "+v"(vm));
+        if (mm >= kInf) mq[e / 4] = (mq[e / 4] & ~at) | nan;
+        if (vm >= kInf) vq[e / 4] = (vq[e / 4] & ~at) | nan;
+      }
+    }
+    store8(t.m, i, n, u32x2_t{mq[0], mq[1]});
+    store8(t.v, i, n, u32x2_t{vq[0], vq[1]});
     if ((threadIdx.x & 15) == 0 && i < n) {
       t.m_scale[i >> 7] = (uint8_t)(ms + 127);
       t.v_scale[i >> 7] = (uint8_t)(vs + 127);
@@ -265,11 +300,18 @@ __global__ __launch_bounds__(256) void k_adamw(const AdamArgs a) {
   }
   if constexpr (MASTER) store_row<float>(t.master, i, n, p);
   if constexpr (RANDOM_P) {
+    uint32_t w[V / 2];
 #pragma unroll
-    for (int e = 0; e < V; ++e)
-      if (finite(p[e])) p[e] = __uint_as_float((__float_as_uint(p[e]) + (r[e] & 0xffffu)) & 0xffff0000u);
+    for (int e = 0; e < V; e += 2) {
+      bf16x2v_t q = {(__bf16)0.0f, (__bf16)0.0f};
+      q = __builtin_amdgcn_cvt_sr_bf16_f32(q, p[e], r[e] << 16, false);
+      q = __builtin_amdgcn_cvt_sr_bf16_f32(q, p[e + 1], r[e + 1] << 16, true);
+      w[e / 2] = __builtin_bit_cast(uint32_t, q);
+    }
+    store_words<P, V>(t.p, i, n, w);
+  } else {
+    store_row<P>(t.p, i, n, p);
   }
-  store_row<P>(t.p, i, n, p);
 }
 
 constexpr int64_t kMaxBlocks = ((int64_t)1 << 24) - 1;   // a launch has below 2^32 threads

@@ -13,9 +13,16 @@ unless ``masters`` keeps fp32 copies of them.
 """
 from __future__ import annotations
 
+import ctypes
+from array import array
+from operator import attrgetter
+
 import torch
 
 from . import abi
+
+_dtype, _shape, _index = attrgetter("dtype"), attrgetter("shape"), torch.Tensor.get_device
+_contiguous, _pointer = torch.Tensor.is_contiguous, torch.Tensor.data_ptr
 
 
 def state_shapes(numel: int, state_bits: int):
@@ -80,6 +87,10 @@ class AdamW:
                 t.m_scale, t.v_scale = self.state["m_scale"][i].data_ptr(), self.state["v_scale"][i].data_ptr()
             if self.masters is not None:
                 t.master = self.masters[i].data_ptr()
+        self._shapes = [p.shape for p in self.params]
+        self._pointers = [p.data_ptr() for p in self.params]
+        words = ctypes.sizeof(abi.AdamwTensor) // 8
+        self._grad_column = memoryview(self._table).cast("B").cast("Q")[abi.AdamwTensor.grad.offset // 8::words]
         self.lr_dev = self.step_dev = None
         if capturable:
             self.lr_dev = torch.full((1,), self.lr, dtype=torch.float32, device=self.device)
@@ -102,22 +113,30 @@ class AdamW:
         one, since the count is stepped there (``step_dev``; ``steps`` counts calls, not replays)."""
         if len(grads) != len(self.params):
             raise ValueError("AdamW: %d gradients for %d parameters" % (len(grads), len(self.params)))
-        table, dtype, device = self._table, grads[0].dtype, self.device
+        dtype, device = grads[0].dtype, self.device
         gcode = abi._dtype_code(grads[0])
-        for i, (g, p) in enumerate(zip(grads, self.params)):
-            if g.dtype != dtype or g.shape != p.shape or not g.is_contiguous() or g.device != device:
-                self._need("gradient", i, g, p.numel(), dtype)
-            t = table[i]
-            t.grad = g.data_ptr()
-            if (t.param or 0) != p.data_ptr():
-                raise ValueError("AdamW: parameter %d has moved" % i)
-        if grad_scale is not None:
-            self._need("grad_scale", 0, grad_scale, 1, torch.float32)
         if device.type != "cuda" or device.index != torch.cuda.current_device():
             raise ValueError("AdamW: the parameters are on %s, not on the current device" % device)
+        # over the lists at once: a loop over the tensors would take longer than their kernel
+        if (list(map(_shape, grads)) != self._shapes or set(map(_dtype, grads)) != {dtype}
+                or set(map(_index, grads)) != {device.index} or not all(map(_contiguous, grads))):
+            for i, (g, p) in enumerate(zip(grads, self.params)):
+                if g.shape != p.shape:
+                    raise ValueError("AdamW: gradient %d is %s, its parameter %s" % (i, tuple(g.shape), tuple(p.shape)))
+                self._need("gradient", i, g, p.numel(), dtype)
+        if list(map(_pointer, self.params)) != self._pointers:
+            raise ValueError("AdamW: a parameter has moved")
+        self._grad_column[:] = memoryview(array("Q", map(_pointer, grads)))
+        if grad_scale is not None:
+            self._need("grad_scale", 0, grad_scale, 1, torch.float32)
         if self.step_dev is not None:
             self.step_dev.add_(1)
-        abi.moe_adamw_step(table, len(self.params), self.dcode, gcode, self.state_bits,
-                           self.lr, self.betas[0], self.betas[1], self.eps, self.steps + 1, self.seed,
-                           grad_scale, self.lr_dev, self.step_dev, stream)
+        try:
+            abi.moe_adamw_step(self._table, len(self.params), self.dcode, gcode, self.state_bits,
+                               self.lr, self.betas[0], self.betas[1], self.eps, self.steps + 1, self.seed,
+                               grad_scale, self.lr_dev, self.step_dev, stream)
+        except abi.MoeError:
+            if self.step_dev is not None:
+                self.step_dev.sub_(1)   # nothing was stepped
+            raise
         self.steps += 1
