@@ -32,6 +32,18 @@ moe_grouped_ffn_fwd_fp8, whose gate/up product reads the rows of a token where
 it loads them; past that call's limits (gather_fits_fp8()) the rows are
 permuted and quantised as R rows.
 
+With ``weight_at_combine`` the expert rows stay unweighted and the top-k
+weights are applied where the rows come back: moe_combine_weighted in place of
+moe_combine, moe_combine_weighted_bwd (which forms the weights' gradient) in
+place of moe_combine_bwd.
+
+``ResidualMoE`` puts a block into a residual stream: the norm of its output,
+a gate, the scaled residual and the norm before the next block in one pass with
+the combine (moe_combine_residual_norm), and moe_residual_norm_bwd before the
+block's backward.  ``MoEBlock.adamw()`` makes the optimizer of a block's
+weights (optim.AdamW), ``MoEBlock.update()`` steps it with the gradients of the
+last backward.
+
 With ``lora_rank`` set the experts are frozen and carry LoRA factors:
 moe_grouped_ffn_fwd_lora / moe_grouped_ffn_bwd_lora replace the grouped-FFN
 calls, and the backward forms the LoRA factor gradients instead of the expert
@@ -51,6 +63,7 @@ from typing import Dict, Optional
 import torch
 
 from . import abi
+from .optim import AdamW
 
 
 def gather_fits(T: int, d: int, k: int) -> bool:
@@ -124,7 +137,10 @@ class MoEBlock:
                  device="cuda", backward: bool = True, fuse_router_dx: bool = True,
                  lora_rank: int = 0, lora_scale: float = 1.0, gather: bool = False,
                  store_x_perm: bool = True, router: Optional[ScoreRouter] = None,
-                 fp8: bool = False):
+                 fp8: bool = False, weight_at_combine: bool = False):
+        if weight_at_combine and gather:
+            raise ValueError("weight_at_combine needs stored rows: gather weights them in its products")
+        self.weight_at_combine = weight_at_combine
         if fp8 and (backward or lora_rank or gather or dtype != torch.bfloat16):
             raise ValueError("fp8 experts run forward only (backward=False), in bf16, without "
                              "LoRA; their rows are gathered by themselves")
@@ -215,6 +231,16 @@ class MoEBlock:
         """bias is added to the logits (it moves selection and weights);
         sel_bias only shifts the scores the top-k compares.  With fp8, w_gu
         and w_down are the pairs of quantize_experts()."""
+        self.forward_rows(x, w_r, w_gu, w_down, bias, noise, stream, sel_bias, lora)
+        if self.weight_at_combine:
+            abi.moe_combine_weighted(self.y_perm, self.slot_to_row, self.topk_w, self.y, stream)
+        else:
+            abi.moe_combine(self.y_perm, self.slot_to_row, self.T, self.k, self.y, stream)
+        return self.y
+
+    def forward_rows(self, x, w_r, w_gu, w_down, bias=None, noise=None, stream=None, sel_bias=None,
+                     lora=None):
+        """forward() up to the experts' rows (y_perm), which are not combined."""
         abi.moe_router_logits(x, w_r, bias, noise, self.logits, stream)
         if self.router is not None:
             self.router.forward(self.logits, sel_bias, self.k, self.topk_idx, self.topk_w, stream)
@@ -224,8 +250,11 @@ class MoEBlock:
             abi.moe_route_biased(self.logits, sel_bias, self.k, self.topk_idx, self.topk_w, stream)
         self.permute(x, stream)
         self.experts_forward(w_gu, w_down, stream, lora, x=x)
-        abi.moe_combine(self.y_perm, self.slot_to_row, self.T, self.k, self.y, stream)
-        return self.y
+
+    @property
+    def row_scale(self):
+        """The weights that the experts' products apply to their rows."""
+        return None if self.weight_at_combine else self.w_perm
 
     def permute(self, x, stream=None):
         if not self.store_x_perm:
@@ -241,7 +270,7 @@ class MoEBlock:
             gathered = not self.store_x_perm
             abi.moe_quant_rows_fp8(x if gathered else self.x_perm, self.x8, self.x8_scale, stream)
             abi.moe_grouped_ffn_fwd_fp8(self.x8, self.x8_scale, self.offsets, *w_gu, *w_down,
-                                        self.w_perm, self.h, self.h_scale, self.y_perm,
+                                        self.row_scale, self.h, self.h_scale, self.y_perm,
                                         row_to_slot=self.row_to_slot if gathered else None,
                                         k=self.k, stream=stream)
             return
@@ -253,11 +282,11 @@ class MoEBlock:
         if self.lora_rank:
             a_gu, b_gu, a_dn, b_dn = lora
             abi.moe_grouped_ffn_fwd_lora(self.x_perm, self.offsets, self.E, w_gu, w_down,
-                                         self.w_perm, a_gu, b_gu, a_dn, b_dn, self.lora_scale,
+                                         self.row_scale, a_gu, b_gu, a_dn, b_dn, self.lora_scale,
                                          self.z_gu, self.z_dn, self.gu, self.h, self.y_perm,
                                          self.ws_ffn, stream)
             return
-        abi.moe_grouped_ffn_fwd(self.x_perm, self.offsets, self.E, w_gu, w_down, self.w_perm,
+        abi.moe_grouped_ffn_fwd(self.x_perm, self.offsets, self.E, w_gu, w_down, self.row_scale,
                                 self.gu, self.h, self.y_perm, self.ws_ffn, stream)
 
     # ------------------------------------------------------------ backward
@@ -271,7 +300,10 @@ class MoEBlock:
         if aux_coeff != 0.0 and self.router is not None and self.router.score != "softmax":
             raise ValueError("aux_coeff: the auxiliary loss is defined on softmax probabilities, "
                              "not on a router's sigmoid scores")
-        if not self.gather:
+        if self.weight_at_combine:
+            abi.moe_combine_weighted_bwd(dy, self.y_perm, self.slot_to_row, self.topk_w, self.dy_perm,
+                                         self.d_row_scale, stream)
+        elif not self.gather:
             abi.moe_combine_bwd(dy, self.slot_to_row, self.k, self.dy_perm, stream)
         self.experts_backward(w_gu, w_down, stream, lora, x=x, dy=dy)
         if self.router is not None:
@@ -305,6 +337,24 @@ class MoEBlock:
         abi.moe_expert_load(self.topk_idx, n, self.E, self.load, self.ws, stream)
         abi.moe_bias_update(self.load, n, self.k, rate, sel_bias, stream)
 
+    def weight_grads(self):
+        """The gradients of the last backward, in the order of adamw()'s weights."""
+        if self.lora_rank:
+            return [self.dw_r, self.da_gu, self.db_gu, self.da_dn, self.db_dn]
+        return [self.dw_r, self.dw_gu, self.dw_down]
+
+    def adamw(self, weights, **options) -> AdamW:
+        """The optimizer of (w_r, w_gu, w_down), or with LoRA of (w_r, a_gu, b_gu, a_dn, b_dn);
+        options as optim.AdamW takes them."""
+        for i, (w, g) in enumerate(zip(weights, self.weight_grads())):
+            if w.shape != g.shape:
+                raise ValueError("adamw: weight %d is %s, its gradient %s" % (i, tuple(w.shape), tuple(g.shape)))
+        return AdamW(weights, **options)
+
+    def update(self, opt: AdamW, grad_scale=None, stream=None):
+        """One optimizer step with the gradients of the last backward."""
+        opt.step(self.weight_grads(), grad_scale, stream)
+
     def experts_backward(self, w_gu, w_down, stream=None, lora=None, x=None, dy=None):
         if self.gather:
             abi.moe_grouped_ffn_bwd_gather(x, dy, self.row_to_slot, self.slot_to_row, self.k,
@@ -314,17 +364,83 @@ class MoEBlock:
                                            self.d_row_scale, self.ws_ffn, stream,
                                            x_perm=self.x_perm)
             return
+        # with weight_at_combine the combine's gradient has formed it
+        d_row_scale = None if self.weight_at_combine else self.d_row_scale
         if self.lora_rank:
             a_gu, b_gu, a_dn, b_dn = lora
             abi.moe_grouped_ffn_bwd_lora(self.x_perm, self.gu, self.h, self.offsets, self.E, w_gu,
-                                         w_down, self.w_perm, self.dy_perm, a_gu, b_gu, a_dn,
+                                         w_down, self.row_scale, self.dy_perm, a_gu, b_gu, a_dn,
                                          b_dn, self.lora_scale, self.z_gu, self.z_dn, self.dgu,
-                                         self.dx_perm, self.d_row_scale, self.da_gu, self.db_gu,
+                                         self.dx_perm, d_row_scale, self.da_gu, self.db_gu,
                                          self.da_dn, self.db_dn, self.ws_ffn, stream)
             return
         abi.moe_grouped_ffn_bwd(self.x_perm, self.gu, self.h, self.offsets, self.E, w_gu,
-                                w_down, self.w_perm, self.dy_perm, self.dgu, self.dx_perm,
-                                self.dw_gu, self.dw_down, self.d_row_scale, self.ws_ffn, stream)
+                                w_down, self.row_scale, self.dy_perm, self.dgu, self.dx_perm,
+                                self.dw_gu, self.dw_down, d_row_scale, self.ws_ffn, stream)
+
+
+class ResidualMoE:
+    """A MoEBlock in a residual stream:
+
+        y = block(n);  out = res_scale x + gate norm(y) w_post;  n_next = norm(out) w_next
+
+    with x the stream and n its norm as the last block (or moe_residual_norm
+    with y None) left it.  w_post and w_next are [d] in the block's dtype, or
+    None without that norm; gate as moe_residual_norm takes it, by its shape.
+    """
+
+    def __init__(self, blk: MoEBlock, post_norm: bool = True, next_norm: bool = True,
+                 res_scale: float = 1.0, eps: float = 1e-6):
+        self.blk, self.res_scale, self.eps = blk, res_scale, eps
+        T, d = blk.T, blk.d
+        z = lambda *s, dt=blk.dtype: torch.empty(*s, dtype=dt, device=blk.device)
+        f32 = torch.float32
+        self.out = z(T, d)
+        self.n = z(T, d) if next_norm else None
+        self.rstd_post = z(T, dt=f32) if post_norm else None
+        self.rstd_next = z(T, dt=f32) if next_norm else None
+        if blk.has_bwd:
+            self.d_x, self.d_y = z(T, d), z(T, d)
+            self.d_w_post = z(d, dt=f32) if post_norm else None
+            self.d_w_next = z(d, dt=f32) if next_norm else None
+            self.d_gate = None
+            self.ws = torch.empty(max(256, abi.moe_residual_norm_bwd_workspace_size(T, d)),
+                                  dtype=torch.uint8, device=blk.device)
+
+    def _check(self, w_post, w_next):
+        if (w_post is None) != (self.rstd_post is None) or (w_next is None) != (self.rstd_next is None):
+            raise ValueError("w_post and w_next go with post_norm and next_norm")
+
+    def forward(self, x, n, w_r, w_gu, w_down, w_post=None, w_next=None, gate=None, stream=None,
+                **routing):
+        """(out, n_next); routing: the other arguments of MoEBlock.forward."""
+        self._check(w_post, w_next)
+        b = self.blk
+        b.forward_rows(n, w_r, w_gu, w_down, stream=stream, **routing)
+        abi.moe_combine_residual_norm(b.y_perm, b.slot_to_row, b.topk_w if b.weight_at_combine else None,
+                                      b.k, x, self.out, self.n, y=b.y if b.has_bwd else None,
+                                      w_post=w_post, w_pre=w_next, gate=gate, res_scale=self.res_scale,
+                                      eps=self.eps, rstd_post=self.rstd_post, rstd_pre=self.rstd_next,
+                                      stream=stream)
+        return self.out, self.n
+
+    def backward(self, n, w_r, w_gu, w_down, d_out, d_n, w_post=None, w_next=None, gate=None,
+                 stream=None, **routing):
+        """d_out: the gradient that reaches out by the stream (None: none), d_n: that of n_next.
+        (d_x, the gradient of n): the first goes on along the stream, the second through the norm
+        that gave n.  Leaves d_w_post, d_w_next and d_gate (fp32 for a gate of [d])."""
+        self._check(w_post, w_next)
+        b = self.blk
+        if gate is not None:
+            dt = torch.float32 if gate.dim() == 1 else gate.dtype
+            if self.d_gate is None or self.d_gate.shape != gate.shape or self.d_gate.dtype != dt:
+                self.d_gate = torch.empty(gate.shape, dtype=dt, device=b.device)
+        abi.moe_residual_norm_bwd(d_out, d_n, self.out, b.y, self.d_x, self.d_y, self.ws, w_post=w_post,
+                                  w_pre=w_next, gate=gate, res_scale=self.res_scale,
+                                  rstd_post=self.rstd_post, rstd_pre=self.rstd_next,
+                                  d_w_post=self.d_w_post, d_w_pre=self.d_w_next,
+                                  d_gate=None if gate is None else self.d_gate, stream=stream)
+        return self.d_x, b.backward(n, w_r, w_gu, w_down, self.d_y, stream=stream, **routing)
 
 
 class ExpertShare:

@@ -1,0 +1,179 @@
+"""The operators around the block as they are used together: ResidualMoE and MoEBlock.update."""
+import numpy as np
+import pytest
+import torch
+
+from mixture_experts_layer_03_amd import abi
+from mixture_experts_layer_03_amd.layer import MoEBlock, ResidualMoE, ScoreRouter
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+BF = torch.bfloat16
+T, D, E, K, F = 333, 256, 8, 3, 128
+
+
+def _weights(seed):
+    g = torch.Generator().manual_seed(seed)
+    r = lambda *s, scale: (torch.randn(*s, generator=g) * scale).to(BF).to(DEV)
+    return {"x": r(T, D, scale=1.0), "n": r(T, D, scale=1.0), "w_r": r(E, D, scale=D ** -0.5),
+            "w_gu": r(E, 2 * F, D, scale=D ** -0.5), "w_down": r(E, D, F, scale=F ** -0.5),
+            "w_post": (1 + 0.2 * torch.randn(D, generator=g)).to(BF).to(DEV),
+            "w_next": (1 + 0.2 * torch.randn(D, generator=g)).to(BF).to(DEV),
+            "gate": r(D, scale=1.0), "d_out": r(T, D, scale=1.0), "d_n": r(T, D, scale=1.0)}
+
+
+def _run(a, at_combine, gate=True, router=None):
+    blk = MoEBlock(T, D, E, K, F, device=DEV, weight_at_combine=at_combine, router=router)
+    res = ResidualMoE(blk, res_scale=0.75, eps=1e-5)
+    gt = a["gate"] if gate else None
+    res.forward(a["x"], a["n"], a["w_r"], a["w_gu"], a["w_down"], a["w_post"], a["w_next"], gt)
+    d_x, d_n = res.backward(a["n"], a["w_r"], a["w_gu"], a["w_down"], a["d_out"], a["d_n"], a["w_post"], a["w_next"], gt)
+    return blk, res, d_x, d_n
+
+
+@pytest.mark.parametrize("at_combine", [False, True])
+def test_it_is_its_calls(at_combine):
+    a = _weights(1)
+    blk, res, d_x, d_n = _run(a, at_combine)
+    keep = {n: getattr(blk, n).clone() for n in ("y", "dx", "dw_r", "dw_gu", "dw_down", "d_topk_w")}
+    ref = MoEBlock(T, D, E, K, F, device=DEV, weight_at_combine=at_combine)
+    y = ref.forward(a["n"], a["w_r"], a["w_gu"], a["w_down"])
+    out, n = torch.empty_like(y), torch.empty_like(y)
+    rp, rn = torch.empty(T, device=DEV), torch.empty(T, device=DEV)
+    abi.moe_residual_norm(a["x"], y, out, n, a["w_post"], a["w_next"], a["gate"], 0.75, 1e-5, rp, rn)
+    assert torch.equal(out, res.out) and torch.equal(n, res.n) and torch.equal(y, keep["y"])
+    gx, gy = torch.empty_like(y), torch.empty_like(y)
+    dwp, dwn, dg = (torch.empty(D, device=DEV) for _ in range(3))
+    abi.moe_residual_norm_bwd(a["d_out"], a["d_n"], out, y, gx, gy, res.ws.clone(), a["w_post"], a["w_next"], a["gate"], 0.75,
+                              rp, rn, dwp, dwn, dg)
+    ref.backward(a["n"], a["w_r"], a["w_gu"], a["w_down"], gy)
+    assert torch.equal(gx, d_x) and torch.equal(dwp, res.d_w_post) and torch.equal(dwn, res.d_w_next) and torch.equal(dg, res.d_gate)
+    for name, t in keep.items():
+        assert torch.equal(t, getattr(ref, name)), name
+
+
+def _rel(a, b):
+    a, b = a.detach().double().cpu(), b.detach().double().cpu()
+    return float((a - b).norm() / b.norm())
+
+
+@pytest.mark.parametrize("router", [None, ScoreRouter("sigmoid", renorm=True, scale=2.0)])
+@pytest.mark.parametrize("at_combine", [False, True])
+def test_gradients_of_the_whole(at_combine, router):
+    """Against 64-bit autograd with the block's own choice of experts.  Between the inputs and any result
+    lie at most 12 stored bf16 tensors (gate/up, h, rows, y, out, n; d_y, its rows, d(gate/up), h again,
+    dx rows, dx), each off by at most 2^-8 of itself; a wrong or missing term is off by about 1."""
+    a = _weights(2)
+    blk, res, d_x, d_n = _run(a, at_combine, router=router)
+    leaf = {n: t.double().cpu().requires_grad_() for n, t in a.items() if n not in ("d_out", "d_n")}
+    idx = blk.topk_idx.long().cpu()
+    logits = leaf["n"] @ leaf["w_r"].t()
+    if router is None:
+        w = torch.softmax(logits.gather(1, idx), 1)
+    else:
+        s = torch.sigmoid(logits).gather(1, idx)
+        w = 2.0 * s / s.sum(1, keepdim=True)
+    y = 0
+    for j in range(K):
+        gu = torch.bmm(leaf["w_gu"][idx[:, j]], leaf["n"][:, :, None])[:, :, 0]
+        h = torch.nn.functional.silu(gu[:, :F]) * gu[:, F:]
+        y = y + w[:, j:j + 1] * torch.bmm(leaf["w_down"][idx[:, j]], h[:, :, None])[:, :, 0]
+    norm = lambda v, g: v * (v.square().mean(1, keepdim=True) + 1e-5).rsqrt() * g
+    out = 0.75 * leaf["x"] + leaf["gate"] * norm(y, leaf["w_post"])
+    n = norm(out, leaf["w_next"])
+    loss = (out * a["d_out"].double().cpu()).sum() + (n * a["d_n"].double().cpu()).sum()
+    loss.backward()
+    bound = 12 * 2.0 ** -8
+    assert _rel(res.out, out) < bound and _rel(res.n, n) < bound
+    got = {"x": d_x, "n": d_n, "w_r": blk.dw_r, "w_gu": blk.dw_gu, "w_down": blk.dw_down, "w_post": res.d_w_post,
+           "w_next": res.d_w_next, "gate": res.d_gate}
+    for name, t in got.items():
+        assert _rel(t, leaf[name].grad) < bound, name
+
+
+def test_weights_at_the_combine_or_in_the_products():
+    """The same block but for one rounding of the rows before or after their weight: 2 bf16 roundings of a
+    row of y, and what they come to in the gradients (as above)."""
+    a = _weights(3)
+    x, _, _, _ = _run(a, False)
+    y, _, _, _ = _run(a, True)
+    assert torch.equal(x.topk_idx, y.topk_idx)
+    for name, bound in (("y", 3 * 2.0 ** -8), ("dx", 12 * 2.0 ** -8), ("dw_gu", 12 * 2.0 ** -8), ("dw_down", 12 * 2.0 ** -8),
+                        ("dw_r", 12 * 2.0 ** -8)):
+        assert _rel(getattr(y, name), getattr(x, name)) < bound, name
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_training_steps_captured(bits):
+    """Forward, backward and AdamW of a block's weights, captured and replayed, against the same steps run eagerly."""
+    a = _weights(4)
+    names = ("w_r", "w_gu", "w_down")
+
+    def setup():
+        w = {n: a[n].clone() for n in names}
+        blk = MoEBlock(T, D, E, K, F, device=DEV, weight_at_combine=True)
+        res = ResidualMoE(blk)
+        opt = blk.adamw([w[n] for n in names], lr=1e-3, weight_decay=[0.0, 0.1, 0.1], state_bits=bits, seed=5, capturable=True)
+        scale = torch.tensor([0.5], device=DEV)
+
+        def step():
+            res.forward(a["x"], a["n"], w["w_r"], w["w_gu"], w["w_down"], a["w_post"], a["w_next"], a["gate"])
+            res.backward(a["n"], w["w_r"], w["w_gu"], w["w_down"], a["d_out"], a["d_n"], a["w_post"], a["w_next"], a["gate"])
+            blk.update(opt, grad_scale=scale)
+        return w, opt, step
+
+    we, oe, eager = setup()
+    wc, oc, cap = setup()
+    eager()
+    cap()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cap()
+    start = {n: t.clone() for n, t in we.items()}
+    for _ in range(3):
+        eager()
+        graph.replay()
+        torch.cuda.synchronize()
+        for n in names:
+            assert torch.equal(we[n], wc[n]), n
+        for n in oe.state:
+            for p, q in zip(oe.state[n], oc.state[n]):
+                assert torch.equal(p.view(torch.uint8), q.view(torch.uint8))
+    for n in names:
+        assert torch.isfinite(we[n]).all() and not torch.equal(we[n], start[n])
+
+
+def test_lora_and_8_bit_experts_with_weights_at_the_combine():
+    a = _weights(5)
+    g = torch.Generator().manual_seed(1)
+    r = 16
+    lora = [(torch.randn(*s, generator=g) * 0.05).to(BF).to(DEV) for s in ((E, r, D), (E, 2 * F, r), (E, r, F), (E, D, r))]
+    got = []
+    for at_combine in (False, True):
+        blk = MoEBlock(T, D, E, K, F, device=DEV, lora_rank=r, weight_at_combine=at_combine)
+        blk.forward(a["n"], a["w_r"], a["w_gu"], a["w_down"], lora=lora)
+        blk.backward(a["n"], a["w_r"], a["w_gu"], a["w_down"], a["d_out"], lora=lora)
+        got.append([t.clone() for t in (blk.y, blk.dx, *blk.weight_grads())])
+    for x, y in zip(*got):
+        assert _rel(y, x) < 12 * 2.0 ** -8
+    from mixture_experts_layer_03_amd.layer import quantize_experts
+    w_gu8, w_down8 = quantize_experts(a["w_gu"], a["w_down"])
+    ys = []
+    for at_combine in (False, True):
+        blk = MoEBlock(T, D, E, K, F, device=DEV, backward=False, fp8=True, weight_at_combine=at_combine)
+        res = ResidualMoE(blk)
+        res.forward(a["x"], a["n"], a["w_r"], w_gu8, w_down8, a["w_post"], a["w_next"])
+        ys.append(res.n.clone())
+    assert _rel(ys[1], ys[0]) < 6 * 2.0 ** -8
+
+
+def test_refusals():
+    with pytest.raises(ValueError):
+        MoEBlock(8, D, E, K, F, device=DEV, gather=True, weight_at_combine=True)
+    blk = MoEBlock(8, D, E, K, F, device=DEV)
+    with pytest.raises(ValueError):
+        blk.adamw([torch.zeros(E, D, device=DEV)] * 3, lr=1e-3)
+    a = _weights(1)
+    with pytest.raises(ValueError):
+        ResidualMoE(blk).forward(a["x"][:8], a["n"][:8], a["w_r"], a["w_gu"], a["w_down"])
