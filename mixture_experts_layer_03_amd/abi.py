@@ -531,34 +531,39 @@ def moe_grouped_ffn_fwd_fp8(x, x_scale, offsets, w_gu, w_gu_scale, w_down, w_dow
         _p(y_perm), _stream(stream)))
 
 
-def _fits(fn, *operands):
-    """Raises for the first (name, tensor, shape, dtype) that is not a contiguous tensor of that
-    shape and type on the current device; None passes."""
-    import torch
-    here = None
-    for name, t, shape, dtype in operands:
-        if t is None:
-            continue
-        if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
-            raise ValueError("%s: %s must be a contiguous %s of %s, not %s of %s%s"
-                             % (fn, name, tuple(shape), dtype, tuple(t.shape), t.dtype,
-                                "" if t.is_contiguous() else " with strides"))
-        at = t.get_device()
-        if here is None:
-            here = torch.cuda.current_device() if at >= 0 else 0
-        if at != here:
-            raise ValueError("%s: %s is on %s, not on the current device" % (fn, name, t.device))
+_torch = None
 
 
-def _gate_kind(fn, gate, T, d, dtype):
+def _types():
+    """(torch, torch.float32, index of the current device); torch is imported by the first call."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch, _torch.float32, _torch._C._cuda_getDevice() if _torch.cuda.is_initialized() else 0
+
+
+def _fits(fn, here, *groups):
+    """Raises for the first tensor that is not a contiguous one of its group's shape and type on the
+    current device; groups: (names, tensors, shape, type), None passes."""
+    for names, tensors, shape, dtype in groups:
+        for t in tensors:
+            if t is not None and (t.shape != shape or t.dtype is not dtype or not t.is_contiguous()
+                                  or t.get_device() != here):
+                name = names.split()[[x is t for x in tensors].index(True)]
+                raise ValueError("%s: %s must be a contiguous %s of %s on the current device, not %s of %s%s on %s"
+                                 % (fn, name, tuple(shape), dtype, tuple(t.shape), t.dtype,
+                                    "" if t.is_contiguous() else " with strides", t.device))
+
+
+def _gate_kind(fn, gate, T, d, dtype, f32):
     """(kind, shape, type) of a gate by its shape: [d] a channel's, [T,1] a token's (fp32), [T,d]."""
-    import torch
     if gate is None:
         return MOE_GATE_NONE, None, None
     if gate.shape == (d,):
         return MOE_GATE_CHANNEL, (d,), dtype
     if gate.shape == (T, 1):
-        return MOE_GATE_TOKEN, (T, 1), torch.float32
+        return MOE_GATE_TOKEN, (T, 1), f32
     if gate.shape == (T, d):
         return MOE_GATE_ELEMENT, (T, d), dtype
     raise ValueError("%s: gate must be [d], [T,1] or [T,d], not %s" % (fn, tuple(gate.shape)))
@@ -567,15 +572,13 @@ def _gate_kind(fn, gate, T, d, dtype):
 def moe_residual_norm(x, y, out, n, w_post=None, w_pre=None, gate=None, res_scale=1.0, eps=1e-6,
                       rstd_post=None, rstd_pre=None, stream=None):
     """y None: n alone, the norm of x.  gate: [d], [T,1] (fp32) or [T,d]."""
-    import torch
+    _, f32, here = _types()
     fn, some = "moe_residual_norm", x if y is None else y
     dt = some.dtype
     T, d = some.shape
-    kind, gshape, gtype = _gate_kind(fn, gate, T, d, dt)
-    row, f32 = (T, d), torch.float32
-    _fits(fn, ("x", x, row, dt), ("y", y, row, dt), ("out", out, row, dt), ("n", n, row, dt),
-          ("w_post", w_post, (d,), dt), ("w_pre", w_pre, (d,), dt), ("gate", gate, gshape, gtype),
-          ("rstd_post", rstd_post, (T,), f32), ("rstd_pre", rstd_pre, (T,), f32))
+    kind, gshape, gtype = _gate_kind(fn, gate, T, d, dt, f32)
+    _fits(fn, here, ("x y out n", (x, y, out, n), (T, d), dt), ("w_post w_pre", (w_post, w_pre), (d,), dt),
+          ("rstd_post rstd_pre", (rstd_post, rstd_pre), (T,), f32), ("gate", (gate,), gshape, gtype))
     _check(fn, lib().moe_residual_norm(
         _p(x), _p(y), _p(gate), kind, _p(w_post), _p(w_pre), res_scale, eps, _dtype_code(some), T, d,
         _p(out), _p(n), _p(rstd_post), _p(rstd_pre), _stream(stream)))
@@ -588,18 +591,16 @@ def moe_residual_norm_bwd_workspace_size(T, d) -> int:
 def moe_residual_norm_bwd(d_out, d_n, out, y, d_x, d_y, ws, w_post=None, w_pre=None, gate=None,
                           res_scale=1.0, rstd_post=None, rstd_pre=None, d_w_post=None,
                           d_w_pre=None, d_gate=None, stream=None):
-    import torch
+    _, f32, here = _types()
     fn, some = "moe_residual_norm_bwd", d_n if d_out is None else d_out
     dt = some.dtype
     T, d = some.shape
-    kind, gshape, gtype = _gate_kind(fn, gate, T, d, dt)
-    row, f32 = (T, d), torch.float32
-    _fits(fn, ("d_out", d_out, row, dt), ("d_n", d_n, row, dt), ("out", out, row, dt),
-          ("y", y, row, dt), ("d_x", d_x, row, dt), ("d_y", d_y, row, dt),
-          ("w_post", w_post, (d,), dt), ("w_pre", w_pre, (d,), dt), ("gate", gate, gshape, gtype),
-          ("rstd_post", rstd_post, (T,), f32), ("rstd_pre", rstd_pre, (T,), f32),
-          ("d_w_post", d_w_post, (d,), f32), ("d_w_pre", d_w_pre, (d,), f32),
-          ("d_gate", d_gate, gshape, f32 if kind == MOE_GATE_CHANNEL else gtype))
+    kind, gshape, gtype = _gate_kind(fn, gate, T, d, dt, f32)
+    _fits(fn, here, ("d_out d_n out y d_x d_y", (d_out, d_n, out, y, d_x, d_y), (T, d), dt),
+          ("w_post w_pre", (w_post, w_pre), (d,), dt), ("gate", (gate,), gshape, gtype),
+          ("rstd_post rstd_pre", (rstd_post, rstd_pre), (T,), f32),
+          ("d_w_post d_w_pre", (d_w_post, d_w_pre), (d,), f32),
+          ("d_gate", (d_gate,), gshape, f32 if kind == MOE_GATE_CHANNEL else gtype))
     _check(fn, lib().moe_residual_norm_bwd(
         _p(d_out), _p(d_n), _p(out), _p(y), _p(gate), kind, _p(w_post), _p(w_pre), _p(rstd_post),
         _p(rstd_pre), res_scale, _dtype_code(some), T, d, _p(d_x), _p(d_y), _p(d_w_post),
@@ -607,26 +608,25 @@ def moe_residual_norm_bwd(d_out, d_n, out, y, d_x, d_y, ws, w_post=None, w_pre=N
 
 
 def moe_combine_weighted(y_perm, slot_to_row, weights, y, stream=None):
-    import torch
-    fn = "moe_combine_weighted"
+    torch, f32, here = _types()
+    fn, dt = "moe_combine_weighted", y.dtype
     T, k = weights.shape
     d = y.shape[1]
-    _fits(fn, ("y_perm", y_perm, (y_perm.shape[0], d), y.dtype), ("y", y, (T, d), y.dtype),
-          ("slot_to_row", slot_to_row, (T * k,), torch.int32), ("weights", weights, (T, k), torch.float32))
+    _fits(fn, here, ("y_perm", (y_perm,), (y_perm.shape[0], d), dt), ("y", (y,), (T, d), dt),
+          ("slot_to_row", (slot_to_row,), (T * k,), torch.int32), ("weights", (weights,), (T, k), f32))
     _check(fn, lib().moe_combine_weighted(_p(y_perm), _p(slot_to_row), _p(weights), _dtype_code(y),
                                           T, d, k, _p(y), _stream(stream)))
 
 
 def moe_combine_weighted_bwd(dy, y_perm, slot_to_row, weights, dy_perm, d_row_scale, stream=None):
-    import torch
-    fn = "moe_combine_weighted_bwd"
+    torch, f32, here = _types()
+    fn, dt = "moe_combine_weighted_bwd", dy.dtype
     T, k = weights.shape
     d = dy.shape[1]
     R = dy_perm.shape[0] if y_perm is None else y_perm.shape[0]
-    _fits(fn, ("dy", dy, (T, d), dy.dtype), ("y_perm", y_perm, (R, d), dy.dtype),
-          ("slot_to_row", slot_to_row, (T * k,), torch.int32),
-          ("weights", weights, (T, k), torch.float32), ("dy_perm", dy_perm, (R, d), dy.dtype),
-          ("d_row_scale", d_row_scale, (R,), torch.float32))
+    _fits(fn, here, ("dy", (dy,), (T, d), dt), ("y_perm dy_perm", (y_perm, dy_perm), (R, d), dt),
+          ("slot_to_row", (slot_to_row,), (T * k,), torch.int32), ("weights", (weights,), (T, k), f32),
+          ("d_row_scale", (d_row_scale,), (R,), f32))
     _check(fn, lib().moe_combine_weighted_bwd(
         _p(dy), _p(y_perm), _p(slot_to_row), _p(weights), _dtype_code(dy), T, d, k, _p(dy_perm),
         _p(d_row_scale), _stream(stream)))
@@ -636,16 +636,14 @@ def moe_combine_residual_norm(y_perm, slot_to_row, weights, k, x, out, n, y=None
                               w_pre=None, gate=None, res_scale=1.0, eps=1e-6, rstd_post=None,
                               rstd_pre=None, stream=None):
     """weights None: the rows carry them already.  y: the combined rows, stored for a backward."""
-    import torch
+    torch, f32, here = _types()
     fn, dt = "moe_combine_residual_norm", out.dtype
     T, d = out.shape
-    kind, gshape, gtype = _gate_kind(fn, gate, T, d, dt)
-    row, f32 = (T, d), torch.float32
-    _fits(fn, ("y_perm", y_perm, (y_perm.shape[0], d), dt),
-          ("slot_to_row", slot_to_row, (T * k,), torch.int32), ("weights", weights, (T, k), f32),
-          ("x", x, row, dt), ("y", y, row, dt), ("out", out, row, dt), ("n", n, row, dt),
-          ("w_post", w_post, (d,), dt), ("w_pre", w_pre, (d,), dt), ("gate", gate, gshape, gtype),
-          ("rstd_post", rstd_post, (T,), f32), ("rstd_pre", rstd_pre, (T,), f32))
+    kind, gshape, gtype = _gate_kind(fn, gate, T, d, dt, f32)
+    _fits(fn, here, ("x y out n", (x, y, out, n), (T, d), dt), ("y_perm", (y_perm,), (y_perm.shape[0], d), dt),
+          ("slot_to_row", (slot_to_row,), (T * k,), torch.int32), ("weights", (weights,), (T, k), f32),
+          ("w_post w_pre", (w_post, w_pre), (d,), dt), ("rstd_post rstd_pre", (rstd_post, rstd_pre), (T,), f32),
+          ("gate", (gate,), gshape, gtype))
     _check(fn, lib().moe_combine_residual_norm(
         _p(y_perm), _p(slot_to_row), _p(weights), k, _p(x), _p(gate), kind, _p(w_post), _p(w_pre),
         res_scale, eps, _dtype_code(out), T, d, _p(y), _p(out), _p(n), _p(rstd_post), _p(rstd_pre),

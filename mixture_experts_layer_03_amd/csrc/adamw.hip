@@ -25,29 +25,27 @@
 namespace moe {
 namespace {
 
-constexpr int kPerLaunch = 40;   // tensors whose pointers fit the kernel's arguments (below 4 KB)
+// Up to kMost tensors of a launch: their pointers fit the kernel's 4 KB of
+// arguments (62 with 8-bit states and no master copies).  A launch costs ~8 us
+// beside its share of the work, most of it its last blocks.
+constexpr int kArgBytes = 4096, kScalarBytes = 96;
+enum { kP, kG, kM, kV, kMore };   // kMore: master, or the scales of m and v behind it
 
-struct AdamTensor {
-  void *p;
-  const void *g;
-  float *master;
-  void *m, *v;
-  uint8_t *m_scale, *v_scale;
-  int64_t n;
-  double decay;                  // the host's 1 - lr wd, or wd where lr is on the device
-  uint32_t index;                // place in the caller's list, for the random bits
-};
-
+template <int PTRS>
 struct AdamArgs {
-  AdamTensor t[kPerLaunch];
-  uint32_t first[kPerLaunch];    // each tensor's first block
+  static constexpr int kMost = (kArgBytes - kScalarBytes) / (8 * PTRS + 16);
+  void *ptr[PTRS][kMost];
+  int64_t n[kMost];
+  float decay[kMost];            // 1 - lr wd, or wd where lr is on the device
+  uint32_t first[kMost];         // each tensor's first block
+  const float *grad_scale, *lr;
+  const int64_t *step_dev;
   int count;
+  uint32_t base;                 // place of the first in the caller's list
   float b1, a1, b2, a2, eps;     // a = 1 - b, rounded from 64 bits
   float step_size, inv_sqrt_bc2; // lr / (1 - b1^t), 1 / sqrt(1 - b2^t)
   float ln_b1, ln_b2;
   uint32_t seed_lo, seed_hi, step;
-  const float *grad_scale, *lr;
-  const int64_t *step_dev;
 };
 
 __device__ __forceinline__ uint32_t mix(uint32_t a) {
@@ -167,29 +165,32 @@ __device__ __forceinline__ void store8(void *base, int64_t i, int64_t n, u32x2_t
 // 4); 8-bit states need the sixth for their arithmetic.
 template <typename P, typename G, bool MASTER, bool EIGHT>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(EIGHT ? 6 : 5, EIGHT ? 6 : 5))) void k_adamw(
-    const AdamArgs a) {
+    const AdamArgs<4 + (MASTER ? 1 : 0) + (EIGHT ? 2 : 0)> a) {
 #pragma clang fp contract(off)
   constexpr int V = EIGHT ? 8 : 4;
   constexpr bool RANDOM_P = sizeof(P) == 2 && !MASTER;
   int lo = 0, hi = a.count - 1;
-  while (lo < hi) {   // the tensor of this block
+  while (lo < hi) {   // the tensor of this block: the last that begins here or before, so none without elements
     const int mid = (lo + hi + 1) >> 1;
     if (a.first[mid] <= blockIdx.x) lo = mid;
     else hi = mid - 1;
   }
-  const AdamTensor &t = a.t[lo];
-  const int64_t n = t.n;
+  const int64_t n = a.n[lo];
   const int64_t i = ((int64_t)(blockIdx.x - a.first[lo]) * 256 + threadIdx.x) * V;
+  void *const t_p = a.ptr[kP][lo], *const t_m = a.ptr[kM][lo], *const t_v = a.ptr[kV][lo];
+  float *const t_master = MASTER ? (float *)a.ptr[MASTER ? kMore : 0][lo] : nullptr;
+  uint8_t *const m_scale = EIGHT ? (uint8_t *)a.ptr[EIGHT ? kMore + MASTER : 0][lo] : nullptr;
+  uint8_t *const v_scale = EIGHT ? (uint8_t *)a.ptr[EIGHT ? kMore + MASTER + 1 : 0][lo] : nullptr;
 
   float g[V], p[V], m[V], v[V];
-  load_row<G>(t.g, i, n, g);
-  if constexpr (MASTER) load_row<float>(t.master, i, n, p);
-  else load_row<P>(t.p, i, n, p);
+  load_row<G>(a.ptr[kG][lo], i, n, g);
+  if constexpr (MASTER) load_row<float>(t_master, i, n, p);
+  else load_row<P>(t_p, i, n, p);
   if constexpr (EIGHT) {
-    const u32x2_t mq = load8(t.m, i, n), vq = load8(t.v, i, n);
+    const u32x2_t mq = load8(t_m, i, n), vq = load8(t_v, i, n);
     const int64_t b = i >> 7;
-    const float ms = i < n ? __uint_as_float((uint32_t)t.m_scale[b] << 23) : 0.0f;
-    const float vs = i < n ? __uint_as_float((uint32_t)t.v_scale[b] << 23) : 0.0f;
+    const float ms = i < n ? __uint_as_float((uint32_t)m_scale[b] << 23) : 0.0f;
+    const float vs = i < n ? __uint_as_float((uint32_t)v_scale[b] << 23) : 0.0f;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const bool up = q & 1;
@@ -203,18 +204,18 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(EIGHT ? 6 :
       v[2 * q + 1] = vf[1] * vs;
     }
   } else {
-    load_row<float>(t.m, i, n, m);
-    load_row<float>(t.v, i, n, v);
+    load_row<float>(t_m, i, n, m);
+    load_row<float>(t_v, i, n, v);
   }
 
   const float gs = a.grad_scale ? *a.grad_scale : 1.0f;
-  float decay = (float)t.decay, step_size = a.step_size, rbc2 = a.inv_sqrt_bc2;
+  float decay = a.decay[lo], step_size = a.step_size, rbc2 = a.inv_sqrt_bc2;
   uint32_t step = a.step;
   if (a.lr) {   // a captured step: the learning rate and the step count are the device's
     const int64_t s = *a.step_dev;
     step = (uint32_t)s;
     const float lr = *a.lr;
-    decay = (float)(1.0 - (double)lr * t.decay);
+    decay = (float)(1.0 - (double)lr * (double)decay);
     step_size = lr / -expm1f((float)s * a.ln_b1);
     rbc2 = 1.0f / sqrtf(-expm1f((float)s * a.ln_b2));
   }
@@ -235,7 +236,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(EIGHT ? 6 :
   uint32_t r[V];
   if constexpr (RANDOM_P || EIGHT) {
     const uint32_t key =
-        mix(mix(mix(mix(a.seed_lo) ^ a.seed_hi) ^ step) ^ t.index) ^ (uint32_t)(i >> 32) ^ (uint32_t)i;
+        mix(mix(mix(mix(a.seed_lo) ^ a.seed_hi) ^ step) ^ (a.base + lo)) ^ (uint32_t)(i >> 32) ^ (uint32_t)i;
 #pragma unroll
     for (int e = 0; e < V; ++e) r[e] = mix(key ^ e);   // i is a multiple of V
   }
@@ -288,17 +289,17 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(EIGHT ? 6 :
         if (vm >= kInf) vq[e / 4] = (vq[e / 4] & ~at) | nan;
       }
     }
-    store8(t.m, i, n, u32x2_t{mq[0], mq[1]});
-    store8(t.v, i, n, u32x2_t{vq[0], vq[1]});
+    store8(t_m, i, n, u32x2_t{mq[0], mq[1]});
+    store8(t_v, i, n, u32x2_t{vq[0], vq[1]});
     if ((threadIdx.x & 15) == 0 && i < n) {
-      t.m_scale[i >> 7] = (uint8_t)(ms + 127);
-      t.v_scale[i >> 7] = (uint8_t)(vs + 127);
+      m_scale[i >> 7] = (uint8_t)(ms + 127);
+      v_scale[i >> 7] = (uint8_t)(vs + 127);
     }
   } else {
-    store_row<float>(t.m, i, n, m);
-    store_row<float>(t.v, i, n, v);
+    store_row<float>(t_m, i, n, m);
+    store_row<float>(t_v, i, n, v);
   }
-  if constexpr (MASTER) store_row<float>(t.master, i, n, p);
+  if constexpr (MASTER) store_row<float>(t_master, i, n, p);
   if constexpr (RANDOM_P) {
     uint32_t w[V / 2];
 #pragma unroll
@@ -308,9 +309,9 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(EIGHT ? 6 :
       q = __builtin_amdgcn_cvt_sr_bf16_f32(q, p[e + 1], r[e + 1] << 16, true);
       w[e / 2] = __builtin_bit_cast(uint32_t, q);
     }
-    store_words<P, V>(t.p, i, n, w);
+    store_words<P, V>(t_p, i, n, w);
   } else {
-    store_row<P>(t.p, i, n, p);
+    store_row<P>(t_p, i, n, p);
   }
 }
 
@@ -335,10 +336,58 @@ bool distinct(const moe_adamw_tensor *t, int n, F of) {
   return std::adjacent_find(all.begin(), all.end()) == all.end();
 }
 
+struct AdamCall {
+  const moe_adamw_tensor *tensors;
+  int n;
+  double lr, beta1, beta2, eps;
+  int64_t step;
+  uint64_t seed;
+  const float *grad_scale, *lr_dev;
+  const int64_t *step_dev;
+};
+
+template <typename P, typename G, bool MASTER, bool EIGHT>
+int run(const char *fn, const AdamCall &c, hipStream_t s) {
+  AdamArgs<4 + (MASTER ? 1 : 0) + (EIGHT ? 2 : 0)> a;
+  static_assert(sizeof(a) <= kArgBytes, "a kernel's arguments");
+  const int64_t per_block = 256 * (EIGHT ? 8 : 4);
+  a.b1 = (float)c.beta1, a.a1 = (float)(1.0 - c.beta1);
+  a.b2 = (float)c.beta2, a.a2 = (float)(1.0 - c.beta2);
+  a.eps = (float)c.eps;
+  a.ln_b1 = (float)std::log(c.beta1), a.ln_b2 = (float)std::log(c.beta2);   // -inf for 0
+  a.step_size = c.lr_dev ? 0.0f : (float)(c.lr / (1.0 - std::pow(c.beta1, (double)c.step)));
+  a.inv_sqrt_bc2 = c.lr_dev ? 0.0f : (float)(1.0 / std::sqrt(1.0 - std::pow(c.beta2, (double)c.step)));
+  a.seed_lo = (uint32_t)c.seed, a.seed_hi = (uint32_t)(c.seed >> 32), a.step = (uint32_t)c.step;
+  a.grad_scale = c.grad_scale, a.lr = c.lr_dev, a.step_dev = c.step_dev;
+  for (int i = 0; i < c.n;) {
+    int64_t blocks = 0;
+    a.count = 0;
+    a.base = (uint32_t)i;
+    for (; i < c.n && a.count < a.kMost; ++i) {
+      const moe_adamw_tensor &t = c.tensors[i];
+      const int64_t mine = (t.numel + per_block - 1) / per_block;
+      if (blocks + mine > kMaxBlocks) break;
+      const int k = a.count++;
+      a.ptr[kP][k] = t.param, a.ptr[kG][k] = const_cast<void *>(t.grad);
+      a.ptr[kM][k] = t.m, a.ptr[kV][k] = t.v;
+      if constexpr (MASTER) a.ptr[kMore][k] = t.master;
+      if constexpr (EIGHT) a.ptr[kMore + MASTER][k] = t.m_scale, a.ptr[kMore + MASTER + 1][k] = t.v_scale;
+      a.n[k] = t.numel;
+      a.decay[k] = (float)(c.lr_dev ? t.weight_decay : 1.0 - c.lr * t.weight_decay);
+      a.first[k] = (uint32_t)blocks;
+      blocks += mine;
+    }
+    if (!blocks) continue;   // tensors without elements
+    MOE_LAUNCH("adamw", s, k_adamw<P, G, MASTER, EIGHT><<<(unsigned)blocks, 256, 0, s>>>(a));
+    const int e = check_launch(fn);
+    if (e != MOE_OK) return e;
+  }
+  return MOE_OK;
+}
+
 template <typename P, typename G, bool MASTER>
-void launch(const AdamArgs &a, unsigned blocks, bool eight, hipStream_t s) {
-  if (eight) k_adamw<P, G, MASTER, true><<<blocks, 256, 0, s>>>(a);
-  else k_adamw<P, G, MASTER, false><<<blocks, 256, 0, s>>>(a);
+int run(const char *fn, const AdamCall &c, bool eight, hipStream_t s) {
+  return eight ? run<P, G, MASTER, true>(fn, c, s) : run<P, G, MASTER, false>(fn, c, s);
 }
 
 }  // namespace
@@ -363,18 +412,20 @@ extern "C" int moe_adamw_step(const moe_adamw_tensor *tensors, int n, int param_
   MOE_REQUIRE(!lr_dev == !step_dev, MOE_ERR_INVALID_ARG, "%s: lr_dev and step_dev go together", fn);
   MOE_REQUIRE(lr_dev || (step >= 1 && step < ((int64_t)1 << 32) && std::isfinite(lr)),
               MOE_ERR_INVALID_ARG, "%s: step=%lld lr=%g", fn, (long long)step, lr);
-  const bool eight = state_bits == 8, master = n > 0 && tensors[0].master;
+  const bool eight = state_bits == 8;
+  bool master = false, first = true;   // of the first tensor with elements
   const int64_t per_block = 256 * (eight ? 8 : 4);
   for (int i = 0; i < n; ++i) {
     const moe_adamw_tensor &t = tensors[i];
     MOE_REQUIRE(t.numel >= 0 && t.numel <= per_block * kMaxBlocks, MOE_ERR_UNSUPPORTED,
                 "%s: tensor %d has %lld elements", fn, i, (long long)t.numel);
-    MOE_REQUIRE((t.master != nullptr) == master && !(master && param_dtype == MOE_F32),
-                MOE_ERR_INVALID_ARG, "%s: tensor %d: all bf16 parameters have a 32-bit copy, or none",
-                fn, i);
     MOE_REQUIRE(std::isfinite(t.weight_decay), MOE_ERR_INVALID_ARG, "%s: tensor %d: weight_decay %g", fn,
                 i, t.weight_decay);
     if (t.numel == 0) continue;
+    if (first) master = t.master, first = false;
+    MOE_REQUIRE((t.master != nullptr) == master && !(master && param_dtype == MOE_F32),
+                MOE_ERR_INVALID_ARG, "%s: tensor %d: all bf16 parameters have a 32-bit copy, or none",
+                fn, i);
     MOE_REQUIRE(t.param && t.grad && t.m && t.v && (!eight || (t.m_scale && t.v_scale)),
                 MOE_ERR_INVALID_ARG, "%s: tensor %d: null pointer", fn, i);
     MOE_REQUIRE(aligned16(t.param) && aligned16(t.grad) && aligned16(t.master) && aligned16(t.m) &&
@@ -392,40 +443,11 @@ extern "C" int moe_adamw_step(const moe_adamw_tensor *tensors, int n, int param_
   }
   MOE_REQUIRE(once, MOE_ERR_INVALID_ARG, "%s: a parameter or state is listed twice", fn);
 
-  AdamArgs a;
-  a.b1 = (float)beta1, a.a1 = (float)(1.0 - beta1), a.b2 = (float)beta2, a.a2 = (float)(1.0 - beta2);
-  a.eps = (float)eps;
-  a.ln_b1 = (float)std::log(beta1), a.ln_b2 = (float)std::log(beta2);   // -inf for 0
-  a.step_size = lr_dev ? 0.0f : (float)(lr / (1.0 - std::pow(beta1, (double)step)));
-  a.inv_sqrt_bc2 = lr_dev ? 0.0f : (float)(1.0 / std::sqrt(1.0 - std::pow(beta2, (double)step)));
-  a.seed_lo = (uint32_t)seed, a.seed_hi = (uint32_t)(seed >> 32), a.step = (uint32_t)step;
-  a.grad_scale = grad_scale, a.lr = lr_dev, a.step_dev = step_dev;
+  const AdamCall c = {tensors, n, lr, beta1, beta2, eps, step, seed, grad_scale, lr_dev, step_dev};
   hipStream_t s = (hipStream_t)stream;
-  for (int i = 0; i < n;) {
-    int64_t blocks = 0;
-    a.count = 0;
-    for (; i < n && a.count < kPerLaunch; ++i) {
-      const moe_adamw_tensor &t = tensors[i];
-      if (t.numel == 0) continue;
-      const int64_t mine = (t.numel + per_block - 1) / per_block;
-      if (blocks + mine > kMaxBlocks) break;
-      a.t[a.count] = {t.param,   t.grad,    t.master, t.m, t.v,
-                      t.m_scale, t.v_scale, t.numel,  lr_dev ? t.weight_decay : 1.0 - lr * t.weight_decay,
-                      (uint32_t)i};
-      a.first[a.count++] = (uint32_t)blocks;
-      blocks += mine;
-    }
-    if (!a.count) break;
-    MOE_LAUNCH("adamw", s, {
-      const unsigned b = (unsigned)blocks;
-      if (param_dtype == MOE_F32) launch<float, float, false>(a, b, eight, s);
-      else if (master && grad_dtype == MOE_F32) launch<bf16_t, float, true>(a, b, eight, s);
-      else if (master) launch<bf16_t, bf16_t, true>(a, b, eight, s);
-      else if (grad_dtype == MOE_F32) launch<bf16_t, float, false>(a, b, eight, s);
-      else launch<bf16_t, bf16_t, false>(a, b, eight, s);
-    });
-    const int e = check_launch(fn);
-    if (e != MOE_OK) return e;
-  }
-  return MOE_OK;
+  if (param_dtype == MOE_F32) return run<float, float, false>(fn, c, eight, s);
+  if (master && grad_dtype == MOE_F32) return run<bf16_t, float, true>(fn, c, eight, s);
+  if (master) return run<bf16_t, bf16_t, true>(fn, c, eight, s);
+  if (grad_dtype == MOE_F32) return run<bf16_t, float, false>(fn, c, eight, s);
+  return run<bf16_t, bf16_t, false>(fn, c, eight, s);
 }

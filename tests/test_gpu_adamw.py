@@ -87,12 +87,15 @@ def test_steps(param, grad, master, bits):
         _check_step(opt, grads, 3e-3, decay, 0.37 if step == 1 else 1.0)
 
 
-def test_more_tensors_than_a_launch_holds():
-    sizes = [1 + 37 * i % 500 for i in range(131)]
-    sizes[50] = 0
+@pytest.mark.parametrize("bits", [8, 32])
+@pytest.mark.parametrize("master", [False, True])
+def test_more_tensors_than_a_launch_holds(master, bits):
+    sizes = [1 + 37 * i % 500 for i in range(231)]
+    for i in (0, 50, 51, 61, 62, 230):          # without elements, at the borders of launches too
+        sizes[i] = 0
     g, params = _params(sizes, torch.bfloat16, 4)
     decay = [0.1] * len(sizes)
-    opt = AdamW(params, lr=1e-2, weight_decay=0.1, state_bits=8, seed=9)
+    opt = AdamW(params, lr=1e-2, weight_decay=0.1, state_bits=bits, masters=True if master else None, seed=9)
     for _ in range(2):
         _check_step(opt, [torch.randn(n, generator=g).to(DEV) for n in sizes], 1e-2, decay)
 
