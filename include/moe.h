@@ -629,7 +629,8 @@ int moe_residual_norm(const void *x, const void *y, const void *gate, int gate_k
  * no output may overlap another tensor.  Sums over t are formed in a fixed
  * order.  T = 0 gives zero weight gradients.  ws:
  * moe_residual_norm_bwd_workspace_size(T,d) bytes, needed for d_w_pre,
- * d_w_post and a channel gate's gradient (MOE_ERR_WORKSPACE if smaller).
+ * d_w_post and a channel gate's gradient (MOE_ERR_WORKSPACE if smaller); calls
+ * that may overlap, also in captured graphs, need one each.
  */
 size_t moe_residual_norm_bwd_workspace_size(int64_t T, int d);
 int moe_residual_norm_bwd(const void *d_out, const void *d_n, const void *out, const void *y,
@@ -644,23 +645,26 @@ int moe_residual_norm_bwd(const void *d_out, const void *d_n, const void *out, c
  * not carry them yet (row_scale NULL in the expert calls):
  *   y[t] = store(sum over j ascending, an fp32 fma chain from +0, of
  *                weights[t*k+j] y_perm[slot_to_row[t*k+j]])
- * A negative slot_to_row entry has no row and adds nothing; what y_perm holds
- * for rows that no slot names is not read.  weights: [T,k] fp32, by slot.
+ * y_perm: [R,d].  A slot_to_row entry outside [0,R) has no row and adds
+ * nothing; what y_perm holds for rows that no slot names is not read.
+ * weights: [T,k] fp32, by slot.
  */
-int moe_combine_weighted(const void *y_perm, const int32_t *slot_to_row, const float *weights,
-                         int dtype, int64_t T, int d, int k, void *y, void *stream);
+int moe_combine_weighted(const void *y_perm, int64_t R, const int32_t *slot_to_row,
+                         const float *weights, int dtype, int64_t T, int d, int k, void *y,
+                         void *stream);
 
 /*
  * Gradient of moe_combine_weighted: for every slot s = t*k+j that has a row r,
  *   dy_perm[r] = store(weights[s] dy[t]),   d_row_scale[r] = <dy[t], y_perm[r]>
- * by row, as moe_route_bwd and moe_route_scored_bwd read it.  Rows that no
+ * by row, as moe_route_bwd and moe_route_scored_bwd read it; y_perm, dy_perm
+ * [R,d], d_row_scale [R].  Rows that no
  * slot names are left as they were.  dy_perm or d_row_scale may be NULL, y_perm too
  * where d_row_scale is; dy_perm may not overlap y_perm.  No two slots may
  * name the same row.  T*k below 2^26.
  */
-int moe_combine_weighted_bwd(const void *dy, const void *y_perm, const int32_t *slot_to_row,
-                             const float *weights, int dtype, int64_t T, int d, int k,
-                             void *dy_perm, float *d_row_scale, void *stream);
+int moe_combine_weighted_bwd(const void *dy, const void *y_perm, int64_t R,
+                             const int32_t *slot_to_row, const float *weights, int dtype, int64_t T,
+                             int d, int k, void *dy_perm, float *d_row_scale, void *stream);
 
 /*
  * moe_combine_weighted (weights NULL: moe_combine) and moe_residual_norm on
@@ -668,10 +672,10 @@ int moe_combine_weighted_bwd(const void *dy, const void *y_perm, const int32_t *
  * rows [T,d], is stored for a backward, or NULL.  Arguments and errors as
  * theirs; y may not overlap another tensor.
  */
-int moe_combine_residual_norm(const void *y_perm, const int32_t *slot_to_row, const float *weights,
-                              int k, const void *x, const void *gate, int gate_kind,
-                              const void *w_post, const void *w_pre, float res_scale, float eps,
-                              int dtype, int64_t T, int d, void *y, void *out, void *n,
+int moe_combine_residual_norm(const void *y_perm, int64_t R, const int32_t *slot_to_row,
+                              const float *weights, int k, const void *x, const void *gate,
+                              int gate_kind, const void *w_post, const void *w_pre, float res_scale,
+                              float eps, int dtype, int64_t T, int d, void *y, void *out, void *n,
                               float *rstd_post, float *rstd_pre, void *stream);
 
 /* ---------------------------------------------------------------- optimizer */
@@ -738,7 +742,9 @@ int moe_adamw_step(const moe_adamw_tensor *tensors, int n, int param_dtype, int 
  * aux_loss_final, lora_proj, lora_transpose, lora_grad,
  * gg_fwd_gate_up_swiglu_gather, gg_bwd_dh_dswiglu_gather, row_scale,
  * gg_bwd_dw_gate_up_gather, route_scored, route_scored_bwd, quant_rows_fp8,
- * quant_weights_fp8, gg_fp8, gg_fp8_gate_up, gg_fp8_down.
+ * quant_weights_fp8, gg_fp8, gg_fp8_gate_up, gg_fp8_down, residual_norm,
+ * combine_residual_norm, residual_norm_bwd, norm_weights, combine_weighted,
+ * combine_weighted_bwd, adamw.
  */
 int moe_timing_enable(int on);
 int moe_timing_reset(void);

@@ -122,11 +122,11 @@ _SIGS = {
                                      _c_void_p, _c_void_p, _c_void_p, _c_void_p, ctypes.c_float,
                                      _i32, _i64, _i32, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
                                      _c_void_p, _c_void_p, _sz, _c_void_p]),
-    "moe_combine_weighted": (_i32, [_c_void_p, _c_void_p, _c_void_p, _i32, _i64, _i32, _i32,
+    "moe_combine_weighted": (_i32, [_c_void_p, _i64, _c_void_p, _c_void_p, _i32, _i64, _i32, _i32,
                                     _c_void_p, _c_void_p]),
-    "moe_combine_weighted_bwd": (_i32, [_c_void_p, _c_void_p, _c_void_p, _c_void_p, _i32, _i64,
-                                        _i32, _i32, _c_void_p, _c_void_p, _c_void_p]),
-    "moe_combine_residual_norm": (_i32, [_c_void_p, _c_void_p, _c_void_p, _i32, _c_void_p,
+    "moe_combine_weighted_bwd": (_i32, [_c_void_p, _c_void_p, _i64, _c_void_p, _c_void_p, _i32,
+                                        _i64, _i32, _i32, _c_void_p, _c_void_p, _c_void_p]),
+    "moe_combine_residual_norm": (_i32, [_c_void_p, _i64, _c_void_p, _c_void_p, _i32, _c_void_p,
                                          _c_void_p, _i32, _c_void_p, _c_void_p, ctypes.c_float,
                                          ctypes.c_float, _i32, _i64, _i32, _c_void_p, _c_void_p,
                                          _c_void_p, _c_void_p, _c_void_p, _c_void_p]),
@@ -614,8 +614,8 @@ def moe_combine_weighted(y_perm, slot_to_row, weights, y, stream=None):
     d = y.shape[1]
     _fits(fn, here, ("y_perm", (y_perm,), (y_perm.shape[0], d), dt), ("y", (y,), (T, d), dt),
           ("slot_to_row", (slot_to_row,), (T * k,), torch.int32), ("weights", (weights,), (T, k), f32))
-    _check(fn, lib().moe_combine_weighted(_p(y_perm), _p(slot_to_row), _p(weights), _dtype_code(y),
-                                          T, d, k, _p(y), _stream(stream)))
+    _check(fn, lib().moe_combine_weighted(_p(y_perm), y_perm.shape[0], _p(slot_to_row), _p(weights),
+                                          _dtype_code(y), T, d, k, _p(y), _stream(stream)))
 
 
 def moe_combine_weighted_bwd(dy, y_perm, slot_to_row, weights, dy_perm, d_row_scale, stream=None):
@@ -628,7 +628,7 @@ def moe_combine_weighted_bwd(dy, y_perm, slot_to_row, weights, dy_perm, d_row_sc
           ("slot_to_row", (slot_to_row,), (T * k,), torch.int32), ("weights", (weights,), (T, k), f32),
           ("d_row_scale", (d_row_scale,), (R,), f32))
     _check(fn, lib().moe_combine_weighted_bwd(
-        _p(dy), _p(y_perm), _p(slot_to_row), _p(weights), _dtype_code(dy), T, d, k, _p(dy_perm),
+        _p(dy), _p(y_perm), R, _p(slot_to_row), _p(weights), _dtype_code(dy), T, d, k, _p(dy_perm),
         _p(d_row_scale), _stream(stream)))
 
 
@@ -645,7 +645,7 @@ def moe_combine_residual_norm(y_perm, slot_to_row, weights, k, x, out, n, y=None
           ("w_post w_pre", (w_post, w_pre), (d,), dt), ("rstd_post rstd_pre", (rstd_post, rstd_pre), (T,), f32),
           ("gate", (gate,), gshape, gtype))
     _check(fn, lib().moe_combine_residual_norm(
-        _p(y_perm), _p(slot_to_row), _p(weights), k, _p(x), _p(gate), kind, _p(w_post), _p(w_pre),
+        _p(y_perm), y_perm.shape[0], _p(slot_to_row), _p(weights), k, _p(x), _p(gate), kind, _p(w_post), _p(w_pre),
         res_scale, eps, _dtype_code(out), T, d, _p(y), _p(out), _p(n), _p(rstd_post), _p(rstd_pre),
         _stream(stream)))
 

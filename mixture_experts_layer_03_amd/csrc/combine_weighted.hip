@@ -17,7 +17,8 @@ template <typename T>
 __global__ __launch_bounds__(256) void k_combine_weighted(const T *__restrict__ y_perm,
                                                           const int32_t *__restrict__ slot_to_row,
                                                           const float *__restrict__ w, int64_t ntok,
-                                                          int d, int k, T *__restrict__ y) {
+                                                          int64_t nrow, int d, int k,
+                                                          T *__restrict__ y) {
   constexpr int N = kVec<T>;
   const int nvec = d / N, parts = (nvec + 64 * kPieces - 1) / (64 * kPieces);
   const int64_t wid = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
@@ -26,7 +27,8 @@ __global__ __launch_bounds__(256) void k_combine_weighted(const T *__restrict__ 
   const int lane = threadIdx.x & 63;
   const uint32_t c0 = (uint32_t)((int)(wid - t * parts) * 64 * kPieces + lane) * 16u;
   const uint32_t bytes = (uint32_t)d * sizeof(T);
-  const int myr = lane < k ? slot_to_row[t * k + lane] : -1;   // k <= 32
+  int myr = lane < k ? slot_to_row[t * k + lane] : -1;   // k <= 32
+  if (myr >= nrow) myr = -1;
   const float myw = myr < 0 ? 0.0f : w[t * k + lane];
   float acc[kPieces][N];
 #pragma unroll
@@ -65,13 +67,13 @@ constexpr int kSteps = 6;   // 16-byte pieces of a row that a lane has in flight
 template <typename T>
 __global__ __launch_bounds__(256) void k_combine_weighted_bwd(
     const T *__restrict__ dy, const T *__restrict__ y_perm, const int32_t *__restrict__ slot_to_row,
-    const float *__restrict__ w, int64_t nslot, int d, int k, T *__restrict__ dy_perm,
+    const float *__restrict__ w, int64_t nslot, int64_t nrow, int d, int k, T *__restrict__ dy_perm,
     float *__restrict__ d_row_scale) {
   constexpr int N = kVec<T>;
   const int64_t slot = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   if (slot >= nslot) return;
   const int r = slot_to_row[slot];
-  if (r < 0) return;
+  if (r < 0 || r >= nrow) return;
   const float wj = w[slot];
   const int lane = threadIdx.x & 63;
   const int64_t t = (int64_t)((uint32_t)slot / (uint32_t)k);   // slots are below 2^31
@@ -104,8 +106,8 @@ __global__ __launch_bounds__(256) void k_combine_weighted_bwd(
   if (lane == 0) d_row_scale[r] = dot;
 }
 
-int check(const char *fn, int64_t T, int d, int k, int dtype) {
-  MOE_REQUIRE(T >= 0, MOE_ERR_INVALID_ARG, "%s: T < 0", fn);
+int check(const char *fn, int64_t T, int64_t R, int d, int k, int dtype) {
+  MOE_REQUIRE(T >= 0 && R >= 0, MOE_ERR_INVALID_ARG, "%s: T or R < 0", fn);
   MOE_REQUIRE(d > 0 && d % 8 == 0, MOE_ERR_UNSUPPORTED, "%s: d=%d not a positive multiple of 8", fn, d);
   MOE_REQUIRE(k >= 1 && k <= kMaxTopK, MOE_ERR_UNSUPPORTED, "%s: k=%d", fn, k);
   MOE_REQUIRE(T < ((int64_t)1 << 31) / k, MOE_ERR_UNSUPPORTED, "%s: T*k >= 2^31", fn);
@@ -118,12 +120,12 @@ int check(const char *fn, int64_t T, int d, int k, int dtype) {
 
 extern "C" {
 
-int moe_combine_weighted(const void *y_perm, const int32_t *slot_to_row, const float *weights,
-                         int dtype, int64_t T, int d, int k, void *y, void *stream) {
+int moe_combine_weighted(const void *y_perm, int64_t R, const int32_t *slot_to_row,
+                         const float *weights, int dtype, int64_t T, int d, int k, void *y, void *stream) {
   using namespace moe;
   const char *fn = "moe_combine_weighted";
   clear_error();
-  const int rc = check(fn, T, d, k, dtype);
+  const int rc = check(fn, T, R, d, k, dtype);
   if (rc != MOE_OK) return rc;
   if (T == 0) return MOE_OK;
   MOE_REQUIRE(y_perm && slot_to_row && weights && y, MOE_ERR_INVALID_ARG, "%s: null pointer", fn);
@@ -136,21 +138,21 @@ int moe_combine_weighted(const void *y_perm, const int32_t *slot_to_row, const f
   MOE_LAUNCH("combine_weighted", s, {
     if (dtype == MOE_BF16)
       k_combine_weighted<bf16_t><<<(unsigned)blocks, 256, 0, s>>>(
-          (const bf16_t *)y_perm, slot_to_row, weights, T, d, k, (bf16_t *)y);
+          (const bf16_t *)y_perm, slot_to_row, weights, T, R, d, k, (bf16_t *)y);
     else
       k_combine_weighted<float><<<(unsigned)blocks, 256, 0, s>>>(
-          (const float *)y_perm, slot_to_row, weights, T, d, k, (float *)y);
+          (const float *)y_perm, slot_to_row, weights, T, R, d, k, (float *)y);
   });
   return check_launch(fn);
 }
 
-int moe_combine_weighted_bwd(const void *dy, const void *y_perm, const int32_t *slot_to_row,
-                             const float *weights, int dtype, int64_t T, int d, int k,
+int moe_combine_weighted_bwd(const void *dy, const void *y_perm, int64_t R,
+                             const int32_t *slot_to_row, const float *weights, int dtype, int64_t T, int d, int k,
                              void *dy_perm, float *d_row_scale, void *stream) {
   using namespace moe;
   const char *fn = "moe_combine_weighted_bwd";
   clear_error();
-  const int rc = check(fn, T, d, k, dtype);
+  const int rc = check(fn, T, R, d, k, dtype);
   if (rc != MOE_OK) return rc;
   if (T == 0) return MOE_OK;
   MOE_REQUIRE(dy && slot_to_row && weights && (dy_perm || d_row_scale) && (y_perm || !d_row_scale),
@@ -164,11 +166,11 @@ int moe_combine_weighted_bwd(const void *dy, const void *y_perm, const int32_t *
   MOE_LAUNCH("combine_weighted_bwd", s, {
     if (dtype == MOE_BF16)
       k_combine_weighted_bwd<bf16_t><<<blocks, 256, 0, s>>>(
-          (const bf16_t *)dy, (const bf16_t *)y_perm, slot_to_row, weights, slots, d, k,
+          (const bf16_t *)dy, (const bf16_t *)y_perm, slot_to_row, weights, slots, R, d, k,
           (bf16_t *)dy_perm, d_row_scale);
     else
       k_combine_weighted_bwd<float><<<blocks, 256, 0, s>>>(
-          (const float *)dy, (const float *)y_perm, slot_to_row, weights, slots, d, k,
+          (const float *)dy, (const float *)y_perm, slot_to_row, weights, slots, R, d, k,
           (float *)dy_perm, d_row_scale);
   });
   return check_launch(fn);

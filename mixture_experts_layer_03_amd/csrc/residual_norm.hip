@@ -58,7 +58,7 @@ struct FwdArgs {
   const float *weights;         // [T,k] or NULL
   void *y_out, *out, *n;
   float *rstd_post, *rstd_pre;
-  int64_t T;
+  int64_t T, R;                 // R: rows of y where it holds expert rows
   int d, k, gate_kind;
   float scale, eps;
 };
@@ -95,7 +95,8 @@ __global__ __launch_bounds__(WIDE ? 1024 : 256) void k_residual_norm(const FwdAr
   };
   if constexpr (GATHER) {
     const int lane = threadIdx.x & 63;
-    const int myr = lane < a.k ? a.slot_to_row[t * a.k + lane] : -1;   // k <= 32
+    int myr = lane < a.k ? a.slot_to_row[t * a.k + lane] : -1;   // k <= 32
+    if (myr >= a.R) myr = -1;
     const float myw = myr < 0 ? 0.0f : a.weights ? a.weights[t * a.k + lane] : 1.0f;
 #pragma unroll
     for (int h = 0; h < NV; ++h)
@@ -318,9 +319,9 @@ __global__ __launch_bounds__(512) void k_residual_norm_bwd(const BwdArgs a) {
       }
     }
     row_sum<true, 3, 8>(s, lds);
-    const float c1 = rn * rn * rn * inv_d * s[0];
+    const float c1 = rn * inv_d * s[0] * rn * rn;   // in this order a row of zeros gives 0
     const float dot = fmaf(-c1, s[2], s[1]);              // sum(A D), without a token's gate
-    const float c2 = a.w_post ? rp * rp * rp * inv_d * r.gt * dot : 0.0f;
+    const float c2 = a.w_post ? rp * inv_d * r.gt * dot * rp * rp : 0.0f;
     if (kToken && a.d_gate && li == 0) ((float *)a.d_gate)[t] = rp * dot;
     const float rpg = rp * r.gt;
     const int64_t row = t * bytes;
@@ -447,8 +448,8 @@ __global__ __launch_bounds__(1024) void k_residual_norm_bwd_long(const BwdArgs a
       }
     }
     row_sum<true, 3>(s, part[flip]);
-    const float c1 = rn * rn * rn * inv_d * s[0], dot = fmaf(-c1, s[2], s[1]);
-    const float c2 = a.w_post ? rp * rp * rp * inv_d * gt * dot : 0.0f, rpg = rp * gt;
+    const float c1 = rn * inv_d * s[0] * rn * rn, dot = fmaf(-c1, s[2], s[1]);
+    const float c2 = a.w_post ? rp * inv_d * gt * dot * rp * rp : 0.0f, rpg = rp * gt;
     if (kToken && a.d_gate && threadIdx.x == 0) ((float *)a.d_gate)[t] = rp * dot;
     const int64_t row = t * a.d;
     for (int c = threadIdx.x; c < nvec; c += 1024) {
@@ -590,8 +591,9 @@ int run_fwd(const char *fn, const FwdArgs &a, bool gather, int dtype, void *stre
   const int rc = check_common(fn, a.T, a.d, dtype, a.gate, a.gate_kind, a.eps);
   if (rc != MOE_OK) return rc;
   if (gather) {
-    MOE_REQUIRE(a.k >= 1 && a.k <= kMaxTopK && a.T * a.k < ((int64_t)1 << 31), MOE_ERR_INVALID_ARG,
-                "%s: bad sizes (T=%lld k=%d)", fn, (long long)a.T, a.k);
+    MOE_REQUIRE(a.R >= 0 && a.k >= 1 && a.k <= kMaxTopK && a.T * a.k < ((int64_t)1 << 31),
+                MOE_ERR_INVALID_ARG, "%s: bad sizes (T=%lld k=%d R=%lld)", fn, (long long)a.T, a.k,
+                (long long)a.R);
   }
   if (a.T == 0) return MOE_OK;   // tensors without elements have no address
   MOE_REQUIRE(!a.n == !a.w_pre, MOE_ERR_INVALID_ARG, "%s: n and w_pre go together", fn);
@@ -630,19 +632,24 @@ int moe_residual_norm(const void *x, const void *y, const void *gate, int gate_k
                       int64_t T, int d, void *out, void *n, float *rstd_post, float *rstd_pre,
                       void *stream) {
   moe::clear_error();
-  const moe::FwdArgs a = {x,   y,         gate,     w_post, w_pre, nullptr, nullptr,   nullptr,   out,
-                          n,   rstd_post, rstd_pre, T,      d,     1,       gate_kind, res_scale, eps};
+  moe::FwdArgs a = {};
+  a.x = x, a.y = y, a.gate = gate, a.gate_kind = gate_kind, a.w_post = w_post, a.w_pre = w_pre;
+  a.scale = res_scale, a.eps = eps, a.T = T, a.d = d;
+  a.out = out, a.n = n, a.rstd_post = rstd_post, a.rstd_pre = rstd_pre;
   return moe::run_fwd("moe_residual_norm", a, false, dtype, stream);
 }
 
-int moe_combine_residual_norm(const void *y_perm, const int32_t *slot_to_row, const float *weights,
-                              int k, const void *x, const void *gate, int gate_kind,
-                              const void *w_post, const void *w_pre, float res_scale, float eps,
-                              int dtype, int64_t T, int d, void *y, void *out, void *n,
+int moe_combine_residual_norm(const void *y_perm, int64_t R, const int32_t *slot_to_row,
+                              const float *weights, int k, const void *x, const void *gate,
+                              int gate_kind, const void *w_post, const void *w_pre, float res_scale,
+                              float eps, int dtype, int64_t T, int d, void *y, void *out, void *n,
                               float *rstd_post, float *rstd_pre, void *stream) {
   moe::clear_error();
-  const moe::FwdArgs a = {x,         y_perm,   gate, w_post, w_pre, slot_to_row, weights, y, out, n,
-                          rstd_post, rstd_pre, T,    d,      k,     gate_kind,   res_scale, eps};
+  moe::FwdArgs a = {};
+  a.x = x, a.y = y_perm, a.gate = gate, a.gate_kind = gate_kind, a.w_post = w_post, a.w_pre = w_pre;
+  a.slot_to_row = slot_to_row, a.weights = weights, a.k = k, a.R = R, a.y_out = y;
+  a.scale = res_scale, a.eps = eps, a.T = T, a.d = d;
+  a.out = out, a.n = n, a.rstd_post = rstd_post, a.rstd_pre = rstd_pre;
   return moe::run_fwd("moe_combine_residual_norm", a, true, dtype, stream);
 }
 

@@ -24,8 +24,8 @@ def _bwd(d_out=P, d_n=P, out=P, y=P, gate=N, kind=0, wp=P, wn=P, rp=P, rn=P, dty
                                            dwn, dg, ws, size, N)
 
 
-def _combine(y_perm=P, rows=P, w=P, k=2, x=P, gate=N, kind=0, T=4, d=64, out=P, n=P):
-    return abi.lib().moe_combine_residual_norm(y_perm, rows, w, k, x, gate, kind, P, P, 1.0, 1e-6, 1, T, d, N, out, n, P, P, N)
+def _combine(y_perm=P, R=8, rows=P, w=P, k=2, x=P, gate=N, kind=0, T=4, d=64, out=P, n=P):
+    return abi.lib().moe_combine_residual_norm(y_perm, R, rows, w, k, x, gate, kind, P, P, 1.0, 1e-6, 1, T, d, N, out, n, P, P, N)
 
 
 @pytest.mark.parametrize("rc,kw", [
@@ -52,7 +52,7 @@ def test_residual_norm_bwd(rc, kw):
 
 @pytest.mark.parametrize("rc,kw", [
     (-1, dict(y_perm=N)), (-1, dict(rows=N)), (-1, dict(k=0)), (-1, dict(k=33)), (-1, dict(out=N)), (-2, dict(d=4)),
-    (-1, dict(n=N)), (-2, dict(T=1 << 30)),
+    (-1, dict(n=N)), (-2, dict(T=1 << 30)), (-1, dict(R=-1)),
 ])
 def test_combine_residual_norm(rc, kw):
     assert _combine(**kw) == rc
@@ -60,19 +60,20 @@ def test_combine_residual_norm(rc, kw):
 
 def test_weighted_combine():
     f, b = abi.lib().moe_combine_weighted, abi.lib().moe_combine_weighted_bwd
-    assert f(P, P, P, 1, -1, 64, 2, P, N) == -1
-    assert f(P, P, P, 1, 4, 63, 2, P, N) == -2
-    assert f(P, P, P, 3, 4, 64, 2, P, N) == -2
-    assert f(P, P, P, 1, 4, 64, 33, P, N) == -2
-    assert f(P, P, N, 1, 4, 64, 2, P, N) == -1
-    assert f(ODD, P, P, 1, 4, 64, 2, P, N) == -1
-    assert f(P, P, P, 1, 1 << 30, 64, 2, P, N) == -2
-    assert f(P, P, P, 1, 1 << 29, 64, 2, P, N) == -2
-    assert f(N, N, N, 1, 0, 64, 2, N, N) == 0
-    assert b(P, P, P, P, 1, 4, 64, 2, N, N, N) == -1
-    assert b(P, N, P, P, 1, 4, 64, 2, P, P, N) == -1
-    assert b(P, P, P, P, 1, 1 << 26, 64, 2, P, P, N) == -2
-    assert b(P, P, P, P, 1, 4, 64, 2, ODD, P, N) == -1
+    assert f(P, 8, P, P, 1, -1, 64, 2, P, N) == -1
+    assert f(P, 8, P, P, 1, 4, 63, 2, P, N) == -2
+    assert f(P, 8, P, P, 3, 4, 64, 2, P, N) == -2
+    assert f(P, 8, P, P, 1, 4, 64, 33, P, N) == -2
+    assert f(P, 8, P, N, 1, 4, 64, 2, P, N) == -1
+    assert f(ODD, 8, P, P, 1, 4, 64, 2, P, N) == -1
+    assert f(P, 8, P, P, 1, 1 << 30, 64, 2, P, N) == -2
+    assert f(P, 8, P, P, 1, 1 << 29, 64, 2, P, N) == -2
+    assert f(P, -1, P, P, 1, 4, 64, 2, P, N) == -1
+    assert f(N, 0, N, N, 1, 0, 64, 2, N, N) == 0
+    assert b(P, P, 8, P, P, 1, 4, 64, 2, N, N, N) == -1
+    assert b(P, N, 8, P, P, 1, 4, 64, 2, P, P, N) == -1
+    assert b(P, P, 8, P, P, 1, 1 << 26, 64, 2, P, P, N) == -2
+    assert b(P, P, 8, P, P, 1, 4, 64, 2, ODD, P, N) == -1
 
 
 def _adamw(change=None, n=2, pd=1, gd=0, bits=8, lr=1e-3, b1=0.9, b2=0.999, eps=1e-8, step=1, lr_dev=N, step_dev=N, tensors=True):
