@@ -78,9 +78,10 @@ __device__ __forceinline__ int block_exponent(uint32_t amax) {
   return amax == 0 ? 0 : max(s, -126);
 }
 
-template <typename T, int V>
+// TAIL: the elements may end here; elsewhere whole vectors, without a branch.
+template <bool TAIL, typename T, int V>
 __device__ __forceinline__ void load_row(const void *base, int64_t i, int64_t n, float (&f)[V]) {
-  if (i + V <= n) {
+  if (!TAIL || i + V <= n) {
     if constexpr (sizeof(T) == 4) {
 #pragma unroll
       for (int q = 0; q < V / 4; ++q) {
@@ -104,13 +105,13 @@ __device__ __forceinline__ void load_row(const void *base, int64_t i, int64_t n,
 }
 
 // V elements as words (two bf16 in one)
-template <typename T, int V>
+template <bool TAIL, typename T, int V>
 __device__ __forceinline__ void store_words(void *base, int64_t i, int64_t n,
                                             const uint32_t (&w)[V * sizeof(T) / 4]) {
   constexpr int kWords = V * (int)sizeof(T) / 4, kEach = kWords < 4 ? kWords : 4;
   typedef uint32_t words __attribute__((ext_vector_type(kEach)));
   T *p = (T *)base + i;
-  if (i + V <= n) {
+  if (!TAIL || i + V <= n) {
 #pragma unroll
     for (int q = 0; q < kWords; q += kEach) {
       words x;
@@ -127,7 +128,7 @@ __device__ __forceinline__ void store_words(void *base, int64_t i, int64_t n,
     else p[e] = (bf16_t)(w[e / 2] >> (16 * (e & 1)));
   }
 }
-template <typename T, int V>
+template <bool TAIL, typename T, int V>
 __device__ __forceinline__ void store_row(void *base, int64_t i, int64_t n, const float (&f)[V]) {
   uint32_t w[V * sizeof(T) / 4];
 #pragma unroll
@@ -135,21 +136,23 @@ __device__ __forceinline__ void store_row(void *base, int64_t i, int64_t n, cons
     if constexpr (sizeof(T) == 4) w[e] = __float_as_uint(f[e]);
     else w[e / 2] = pack_bf16x2(f[e], f[e + 1]);
   }
-  store_words<T, V>(base, i, n, w);
+  store_words<TAIL, T, V>(base, i, n, w);
 }
 
+template <bool TAIL>
 __device__ __forceinline__ u32x2_t load8(const void *base, int64_t i, int64_t n) {
   const uint8_t *p = (const uint8_t *)base + i;
-  if (i + 8 <= n) return __builtin_nontemporal_load(reinterpret_cast<const u32x2_t *>(p));
+  if (!TAIL || i + 8 <= n) return __builtin_nontemporal_load(reinterpret_cast<const u32x2_t *>(p));
   u32x2_t w = {0u, 0u};
 #pragma unroll
   for (int e = 0; e < 8; ++e)
     if (i + e < n) w[e / 4] |= (uint32_t)p[e] << (8 * (e & 3));
   return w;
 }
+template <bool TAIL>
 __device__ __forceinline__ void store8(void *base, int64_t i, int64_t n, u32x2_t w) {
   uint8_t *p = (uint8_t *)base + i;
-  if (i + 8 <= n) {
+  if (!TAIL || i + 8 <= n) {
     __builtin_nontemporal_store(w, reinterpret_cast<u32x2_t *>(p));
     return;
   }
@@ -160,37 +163,26 @@ __device__ __forceinline__ void store8(void *base, int64_t i, int64_t n, u32x2_t
 
 // P, G: types of parameter and gradient.  A thread takes V neighbouring
 // elements, a block 256 V of them; 16 lanes share the scale of 128 (i >> 7).
-// Five waves a SIMD with 32-bit states: more of them have more lines under way
-// than HBM serves in order (30 bytes an element: 6.3 TB/s with 5, 6.1 with 8 or
-// 4); 8-bit states need the sixth for their arithmetic.
-template <typename P, typename G, bool MASTER, bool EIGHT>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(EIGHT ? 6 : 5, EIGHT ? 6 : 5))) void k_adamw(
-    const AdamArgs<4 + (MASTER ? 1 : 0) + (EIGHT ? 2 : 0)> a) {
+template <typename P, typename G, bool MASTER, bool EIGHT, bool TAIL>
+__device__ __forceinline__ void adamw_block(const AdamArgs<4 + (MASTER ? 1 : 0) + (EIGHT ? 2 : 0)> &a,
+                                            int lo, int64_t i, int64_t n) {
 #pragma clang fp contract(off)
   constexpr int V = EIGHT ? 8 : 4;
   constexpr bool RANDOM_P = sizeof(P) == 2 && !MASTER;
-  int lo = 0, hi = a.count - 1;
-  while (lo < hi) {   // the tensor of this block: the last that begins here or before, so none without elements
-    const int mid = (lo + hi + 1) >> 1;
-    if (a.first[mid] <= blockIdx.x) lo = mid;
-    else hi = mid - 1;
-  }
-  const int64_t n = a.n[lo];
-  const int64_t i = ((int64_t)(blockIdx.x - a.first[lo]) * 256 + threadIdx.x) * V;
   void *const t_p = a.ptr[kP][lo], *const t_m = a.ptr[kM][lo], *const t_v = a.ptr[kV][lo];
   float *const t_master = MASTER ? (float *)a.ptr[MASTER ? kMore : 0][lo] : nullptr;
   uint8_t *const m_scale = EIGHT ? (uint8_t *)a.ptr[EIGHT ? kMore + MASTER : 0][lo] : nullptr;
   uint8_t *const v_scale = EIGHT ? (uint8_t *)a.ptr[EIGHT ? kMore + MASTER + 1 : 0][lo] : nullptr;
 
   float g[V], p[V], m[V], v[V];
-  load_row<G>(a.ptr[kG][lo], i, n, g);
-  if constexpr (MASTER) load_row<float>(t_master, i, n, p);
-  else load_row<P>(t_p, i, n, p);
+  load_row<TAIL, G>(a.ptr[kG][lo], i, n, g);
+  if constexpr (MASTER) load_row<TAIL, float>(t_master, i, n, p);
+  else load_row<TAIL, P>(t_p, i, n, p);
   if constexpr (EIGHT) {
-    const u32x2_t mq = load8(t_m, i, n), vq = load8(t_v, i, n);
+    const u32x2_t mq = load8<TAIL>(t_m, i, n), vq = load8<TAIL>(t_v, i, n);
     const int64_t b = i >> 7;
-    const float ms = i < n ? __uint_as_float((uint32_t)m_scale[b] << 23) : 0.0f;
-    const float vs = i < n ? __uint_as_float((uint32_t)v_scale[b] << 23) : 0.0f;
+    const float ms = !TAIL || i < n ? __uint_as_float((uint32_t)m_scale[b] << 23) : 0.0f;
+    const float vs = !TAIL || i < n ? __uint_as_float((uint32_t)v_scale[b] << 23) : 0.0f;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const bool up = q & 1;
@@ -204,8 +196,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(EIGHT ? 6 :
       v[2 * q + 1] = vf[1] * vs;
     }
   } else {
-    load_row<float>(t_m, i, n, m);
-    load_row<float>(t_v, i, n, v);
+    load_row<TAIL, float>(t_m, i, n, m);
+    load_row<TAIL, float>(t_v, i, n, v);
   }
 
   const float gs = a.grad_scale ? *a.grad_scale : 1.0f;
@@ -289,17 +281,17 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(EIGHT ? 6 :
         if (vm >= kInf) vq[e / 4] = (vq[e / 4] & ~at) | nan;
       }
     }
-    store8(t_m, i, n, u32x2_t{mq[0], mq[1]});
-    store8(t_v, i, n, u32x2_t{vq[0], vq[1]});
-    if ((threadIdx.x & 15) == 0 && i < n) {
+    store8<TAIL>(t_m, i, n, u32x2_t{mq[0], mq[1]});
+    store8<TAIL>(t_v, i, n, u32x2_t{vq[0], vq[1]});
+    if ((threadIdx.x & 15) == 0 && (!TAIL || i < n)) {
       m_scale[i >> 7] = (uint8_t)(ms + 127);
       v_scale[i >> 7] = (uint8_t)(vs + 127);
     }
   } else {
-    store_row<float>(t_m, i, n, m);
-    store_row<float>(t_v, i, n, v);
+    store_row<TAIL, float>(t_m, i, n, m);
+    store_row<TAIL, float>(t_v, i, n, v);
   }
-  if constexpr (MASTER) store_row<float>(t_master, i, n, p);
+  if constexpr (MASTER) store_row<TAIL, float>(t_master, i, n, p);
   if constexpr (RANDOM_P) {
     uint32_t w[V / 2];
 #pragma unroll
@@ -309,10 +301,34 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(EIGHT ? 6 :
       q = __builtin_amdgcn_cvt_sr_bf16_f32(q, p[e + 1], r[e + 1] << 16, true);
       w[e / 2] = __builtin_bit_cast(uint32_t, q);
     }
-    store_words<P, V>(t_p, i, n, w);
+    store_words<TAIL, P, V>(t_p, i, n, w);
   } else {
-    store_row<P>(t_p, i, n, p);
+    store_row<TAIL, P>(t_p, i, n, p);
   }
+}
+
+// Five waves a SIMD with 32-bit states: more of them have more lines under way
+// than HBM serves in order (30 bytes an element: 6.3 TB/s with 5, 6.1 with 8 or
+// 4); 8-bit states need the sixth for their arithmetic.
+template <typename P, typename G, bool MASTER, bool EIGHT>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(EIGHT ? 6 : 5, EIGHT ? 6 : 5))) void k_adamw(
+    const AdamArgs<4 + (MASTER ? 1 : 0) + (EIGHT ? 2 : 0)> a) {
+  constexpr int V = EIGHT ? 8 : 4;
+  int lo = 0, hi = a.count - 1;
+  while (lo < hi) {   // the tensor of this block: the last that begins here or before, so none without elements
+    const int mid = (lo + hi + 1) >> 1;
+    if (a.first[mid] <= blockIdx.x) lo = mid;
+    else hi = mid - 1;
+  }
+  const int64_t n = a.n[lo], at = (int64_t)(blockIdx.x - a.first[lo]) * 256 * V;
+  const int64_t i = at + threadIdx.x * V;
+  // Whole blocks without the code for ends between their accesses: 8-bit
+  // states' instructions are then half as many to fetch when a launch begins
+  // (120 tensors of 28M elements 106 -> 95 us).  With 32-bit states the
+  // branches between the accesses spread them out, and long tensors take 3.80
+  // ms with them, 3.98 without (796M elements).
+  if (EIGHT && at + 256 * V <= n) adamw_block<P, G, MASTER, EIGHT, false>(a, lo, i, n);
+  else adamw_block<P, G, MASTER, EIGHT, true>(a, lo, i, n);
 }
 
 constexpr int64_t kMaxBlocks = ((int64_t)1 << 24) - 1;   // a launch has below 2^32 threads
