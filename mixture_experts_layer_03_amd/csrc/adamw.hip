@@ -1,4 +1,4 @@
-// An AdamW step over many tensors in one launch for each 40 of them.
+// An AdamW step over many tensors in a launch for each 55 to 83 of them.
 //
 //   m = b1 m + (1-b1) g,  v = b2 v + (1-b2) g g,
 //   p = p (1 - lr wd) - lr/(1-b1^t) m / (sqrt(v)/sqrt(1-b2^t) + eps)
@@ -12,8 +12,10 @@
 // reason.  The random bits are a hash of (seed, step, tensor, element).
 //
 // Per element 28 bytes move with fp32 parameters, 30 with bf16 ones and a
-// copy, 12 with bf16 ones and 8-bit states: HBM bounds the step, with the
-// hash and roundings (~100 instructions an element) close behind at 12.
+// copy, 12 with bf16 ones and 8-bit states, each once and in order: HBM bounds
+// the step.  Measured: 796M bf16 weights with copies 3.78 ms (6.3 TB/s), 604M
+// with 8-bit states 1.16 ms (6.3 TB/s; ~48 instructions an element, five of
+// them at quarter rate).
 #include <algorithm>
 #include <cmath>
 #include <functional>
@@ -26,8 +28,9 @@ namespace moe {
 namespace {
 
 // Up to kMost tensors of a launch: their pointers fit the kernel's 4 KB of
-// arguments (62 with 8-bit states and no master copies).  A launch costs ~8 us
-// beside its share of the work, most of it its last blocks.
+// arguments (62 with 8-bit states and no master copies).  A launch costs 5 to
+// 10 us beside its share of the work: its first blocks' way to the code and
+// its last blocks.
 constexpr int kArgBytes = 4096, kScalarBytes = 96;
 enum { kP, kG, kM, kV, kMore };   // kMore: master, or the scales of m and v behind it
 

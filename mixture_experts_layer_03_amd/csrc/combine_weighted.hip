@@ -11,7 +11,8 @@
 namespace moe {
 namespace {
 
-// One wave for kPieces x 64 16-byte pieces of a token's row, four expert rows in flight.
+// One wave for kPieces x 64 16-byte pieces of a token's row, four expert rows in
+// flight, so that several waves share a token whose rows come from far apart.
 constexpr int kPieces = 2;
 template <typename T>
 __global__ __launch_bounds__(256) void k_combine_weighted(const T *__restrict__ y_perm,
@@ -62,8 +63,12 @@ __global__ __launch_bounds__(256) void k_combine_weighted(const T *__restrict__ 
 }
 
 // One wave for each slot; the waves of a token's slots lie next to each other,
-// so that its row of dy comes from HBM once.
-constexpr int kSteps = 6;   // 16-byte pieces of a row that a lane has in flight
+// so that its row of dy comes from HBM once (read past the caches it would
+// take 171 us where it takes 162).  16384 tokens with 4 rows of 2880 (850 MB):
+// 150 to 170 us as cards differ; with the rows in slot order 142, so it is the
+// order of the rows that HBM is slower with.  A wave for each token, which
+// keeps dy in registers, takes 169.
+constexpr int kSteps = 6;   // 16-byte pieces of a row that a lane has in flight (3: 164 us)
 template <typename T>
 __global__ __launch_bounds__(256) void k_combine_weighted_bwd(
     const T *__restrict__ dy, const T *__restrict__ y_perm, const int32_t *__restrict__ slot_to_row,

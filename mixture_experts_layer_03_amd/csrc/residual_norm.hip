@@ -10,6 +10,8 @@
 //   n   = store(out r(out) w_pre), of the stored out: the backward has no other
 // A pass moves x, z, out and n once (or k rows in z's place) and does ~10
 // operations an element: HBM bounds it, launch latency for few rows.
+// Measured, bf16: 32768 rows of 2880 (755 MB) 130 us, 5.8 TB/s; 8 expert rows
+// of 2048 for each of 32768 tokens (1.48 GB) 254 us, 5.8 TB/s; 16 rows 4 us.
 #include <algorithm>
 
 #include "rows.h"
@@ -64,7 +66,10 @@ struct FwdArgs {
 };
 
 // One row for each wave (four in a block), or with WIDE one for a block of
-// up to 16 waves.  A lane holds NV pieces of 16 bytes of the row.
+// up to 16 waves.  A lane holds NV pieces of 16 bytes of the row, from one read
+// to the last write.  A wave has no barriers (32768 rows of 2880: 130 us, a
+// block for each 140); a block spreads a row where waves would not fill the
+// card or a row does not fit their registers.
 template <typename T, int NV, bool WIDE, bool GATHER>
 __global__ __launch_bounds__(WIDE ? 1024 : 256) void k_residual_norm(const FwdArgs a) {
   constexpr int N = kVec<T>;
@@ -91,7 +96,7 @@ __global__ __launch_bounds__(WIDE ? 1024 : 256) void k_residual_norm(const FwdAr
 #pragma unroll
     for (int h = 0; h < NV; ++h) xv[h] = x.load(c[h]);
 #pragma unroll
-    for (int h = 0; h < NV; ++h) gv[h] = g.load(c[h]);
+    for (int h = 0; h < NV; ++h) gv[h] = g.keep(c[h]);   // a channel's is every row's
   };
   if constexpr (GATHER) {
     const int lane = threadIdx.x & 63;
@@ -693,7 +698,7 @@ int moe_residual_norm_bwd(const void *d_out, const void *d_n, const void *out, c
               MOE_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", fn);
   hipStream_t s = (hipStream_t)stream;
   BwdArgs a = {};
-  a.d_out = d_out, a.d_n = d_n, a.out = out, a.y = y, a.gate = gate, a.w_post = w_post, a.w_pre = w_pre;
+  a.d_out = d_out, a.d_n = d_n, a.out = out, a.y = w_post || d_gate ? y : nullptr, a.gate = gate, a.w_post = w_post, a.w_pre = w_pre;
   a.rstd_post = w_post ? rstd_post : nullptr, a.rstd_pre = w_pre ? rstd_pre : nullptr;
   a.d_x = d_x, a.d_y = d_y, a.d_gate = d_gate, a.partial = (float *)ws;
   a.T = T, a.d = d, a.gate_kind = gate_kind, a.columns = columns, a.scale = res_scale;

@@ -1,4 +1,4 @@
-"""AdamW over the tensors of a model, one launch for each 40 of them.
+"""AdamW over the tensors of a model, one launch for dozens of them.
 
 ``AdamW`` keeps the states and the step count of a list of parameters and
 issues moe_adamw_step (include/moe.h has the arithmetic):

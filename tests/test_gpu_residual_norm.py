@@ -182,20 +182,21 @@ def test_combine_residual_norm_is_the_two_calls(T, d, k, dtype, weighted):
     assert torch.equal(outs[0][0][0], (0.5 * x[0].float()).to(dt))
 
 
-def test_norm_alone_and_in_place():
-    g, x, y, wp, wn, _ = _inputs(37, 2880, torch.bfloat16, True, True, "none", 9)
-    n, rn = torch.empty_like(x), torch.empty(37, device=DEV)
+@pytest.mark.parametrize("T", [37, 2051])
+def test_norm_alone_and_in_place(T):
+    g, x, y, wp, wn, _ = _inputs(T, 2880, torch.bfloat16, True, True, "none", 9)
+    n, rn = torch.empty_like(x), torch.empty(T, device=DEV)
     abi.moe_residual_norm(x, None, None, n, w_pre=wn, eps=1e-5, rstd_pre=rn)
     r = O.rstd(_np(x), 1e-5)
     ref = _np(x) * r * _np(wn)
     _close("n", n, ref, (_u(x.dtype) * 1.01 + 52 * V) * abs(ref))
-    d_n, d_x, dw = _rand(g, 37, 2880, dt=x.dtype), torch.empty_like(x), torch.empty(2880, device=DEV)
-    ws = torch.empty(abi.moe_residual_norm_bwd_workspace_size(37, 2880), dtype=torch.uint8, device=DEV)
-    for d_out in (None, _rand(g, 37, 2880, dt=x.dtype)):
+    d_n, d_x, dw = _rand(g, T, 2880, dt=x.dtype), torch.empty_like(x), torch.empty(2880, device=DEV)
+    ws = torch.empty(abi.moe_residual_norm_bwd_workspace_size(T, 2880), dtype=torch.uint8, device=DEV)
+    for d_out in (None, _rand(g, T, 2880, dt=x.dtype)):
         abi.moe_residual_norm_bwd(d_out, d_n, x, None, d_x, None, ws, w_pre=wn, rstd_pre=rn, d_w_pre=dw)
-        ref = O.residual_norm_bwd(_np(d_out), _np(d_n), _np(x), np.zeros((37, 2880)), None, _np(wn), None, 1.0, None, _np(rn)[:, None])
+        ref = O.residual_norm_bwd(_np(d_out), _np(d_n), _np(x), np.zeros((T, 2880)), None, _np(wn), None, 1.0, None, _np(rn)[:, None])
         _close("d_x", d_x, ref["d_x"][0], _u(x.dtype) * 1.01 * abs(ref["d_x"][0]) + 128 * V * ref["d_x"][1])
-        _close("d_w_pre", dw, ref["d_w_pre"][0], 200 * V * ref["d_w_pre"][1])
+        _close("d_w_pre", dw, ref["d_w_pre"][0], (T / 256 + 209 + 128) * V * ref["d_w_pre"][1])
     # out over x, n over y, d_x over d_out
     out, n2 = torch.empty_like(x), torch.empty_like(x)
     abi.moe_residual_norm(x, y, out, n2, wp, wn)
@@ -204,6 +205,36 @@ def test_norm_alone_and_in_place():
     assert torch.equal(out, x2) and torch.equal(n2, y2)
     abi.moe_residual_norm_bwd(d_out, d_n, x, None, d_out, None, ws, w_pre=wn, rstd_pre=rn)
     assert torch.equal(d_out, d_x)
+
+
+def test_gradient_of_zero_rows_with_a_tiny_eps():
+    """1/rms is 1e15 there: d_x = scale (d_out + rn d_n w), and no product of three of it overflows against a zero."""
+    T, d = 5, 264
+    g, x, y, wp, wn, _ = _inputs(T, d, torch.float32, True, True, "none", 4)
+    x[2], y[3] = 0.0, 0.0
+    rp, rn = (torch.tensor(O.rstd(_np(t), 1e-30)[:, 0]).float().to(DEV) for t in (y, x))
+    go, gn = _rand(g, T, d), _rand(g, T, d)
+    d_x, d_y = torch.empty_like(x), torch.empty_like(x)
+    abi.moe_residual_norm_bwd(go, gn, x, y, d_x, d_y, None, wp, wn, None, 1.0, rp, rn)
+    ref = O.residual_norm_bwd(_np(go), _np(gn), _np(x), _np(y), _np(wp), _np(wn), None, 1.0, _np(rp)[:, None], _np(rn)[:, None])
+    for name, t in (("d_x", d_x), ("d_y", d_y)):
+        v, size = ref[name]
+        _close(name, t, v, V * abs(v) + 128 * V * size)
+
+
+def test_what_is_not_needed_is_not_read():
+    T, d = 6, 520
+    g, x, _, _, wn, gt = _inputs(T, d, torch.bfloat16, False, True, "channel", 4)
+    nan = torch.full_like(x, float("nan"))
+    rn = torch.tensor(O.rstd(_np(x), 1e-5)[:, 0]).float().to(DEV)
+    go, gn = _rand(g, T, d, dt=x.dtype), _rand(g, T, d, dt=x.dtype)
+    a, b = [torch.empty_like(x) for _ in range(2)], [torch.empty_like(x) for _ in range(2)]
+    abi.moe_residual_norm_bwd(go, gn, x, nan, a[0], a[1], None, None, wn, gt, 1.0, None, rn)
+    abi.moe_residual_norm_bwd(go, gn, x, None, b[0], b[1], None, None, wn, gt, 1.0, None, rn)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]) and torch.isfinite(a[1]).all()
+    c = torch.empty_like(x)      # without the second norm, out is not read
+    abi.moe_residual_norm_bwd(go, None, nan, None, c, None, None, None, None, gt, 0.5)
+    assert torch.equal(c, (0.5 * go.float()).to(c.dtype))
 
 
 def test_rows_that_are_zero_inf_or_nan_stay_alone():
