@@ -99,12 +99,12 @@ def _mix(a):
     return a ^ (a >> np.uint64(16))
 
 
-def random_bits(seed, step, tensor, n):
-    """(low half of r, high half of r, high half of r * C) of n elements."""
+def random_bits(seed, step, tensor, n, start=0):
+    """(low half of r, high half of r, high half of r * C) of n elements from `start` on."""
     m32 = np.uint64(0xFFFFFFFF)
-    e = np.arange(n, dtype=np.uint64)
+    e = np.arange(start, start + n, dtype=np.uint64)
     key = _mix(_mix(_mix(_mix(seed & 0xFFFFFFFF) ^ np.uint64(seed >> 32)) ^ np.uint64(step)) ^ np.uint64(tensor))
-    r = _mix(key ^ (e >> np.uint64(32)) ^ (e & m32))
+    r = _mix((key ^ (e >> np.uint64(32))) ^ (e & m32))
     r2 = (r * np.uint64(0x30E9132D)) & m32
     return r & np.uint64(0xFFFF), r >> np.uint64(16), r2 >> np.uint64(16)
 
