@@ -168,6 +168,20 @@ def test_lora_and_8_bit_experts_with_weights_at_the_combine():
     assert _rel(ys[1], ys[0]) < 6 * 2.0 ** -8
 
 
+def test_gathered_rows():
+    """The arrangement whose products read token rows gives the same stream and gradients, bit for bit."""
+    a = _weights(6)
+    got = []
+    for gather in (False, True):
+        blk = MoEBlock(T, D, E, K, F, device=DEV, gather=gather)
+        res = ResidualMoE(blk)
+        res.forward(a["x"], a["n"], a["w_r"], a["w_gu"], a["w_down"], a["w_post"], a["w_next"])
+        d_x, d_n = res.backward(a["n"], a["w_r"], a["w_gu"], a["w_down"], a["d_out"], a["d_n"], a["w_post"], a["w_next"])
+        got.append([t.clone() for t in (res.out, res.n, d_x, d_n, res.d_w_post, res.d_w_next, *blk.weight_grads())])
+    for x, y in zip(*got):
+        assert torch.equal(x, y)
+
+
 def test_refusals():
     with pytest.raises(ValueError):
         MoEBlock(8, D, E, K, F, device=DEV, gather=True, weight_at_combine=True)

@@ -222,6 +222,24 @@ def test_gradient_of_zero_rows_with_a_tiny_eps():
         _close(name, t, v, V * abs(v) + 128 * V * size)
 
 
+@pytest.mark.parametrize("T", [6, 2050])
+def test_without_a_stream(T):
+    """x None: out = gate norm(y) w_post, and no d_x."""
+    d = 776
+    g, _, y, wp, wn, gt = _inputs(T, d, torch.bfloat16, True, True, "token", 8)
+    out, n, z = (torch.empty_like(y) for _ in range(3))
+    rp, rn = torch.empty(T, device=DEV), torch.empty(T, device=DEV)
+    abi.moe_residual_norm(None, y, out, n, wp, wn, gt, 0.75, 1e-5, rp, rn)
+    _check_forward(torch.zeros_like(y), y, out, n, rp, rn, wp, wn, gt, 0.75, 1e-5)
+    abi.moe_residual_norm(torch.zeros_like(y), y, z, n, wp, wn, gt, 0.75, 1e-5)
+    assert torch.equal(out, z)
+    go, gn = _rand(g, T, d, dt=y.dtype), _rand(g, T, d, dt=y.dtype)
+    a, b, dx = (torch.empty_like(y) for _ in range(3))
+    abi.moe_residual_norm_bwd(go, gn, out, y, None, a, None, wp, wn, gt, 0.75, rp, rn)
+    abi.moe_residual_norm_bwd(go, gn, out, y, dx, b, None, wp, wn, gt, 0.75, rp, rn)
+    assert torch.equal(a, b)
+
+
 def test_what_is_not_needed_is_not_read():
     T, d = 6, 520
     g, x, _, _, wn, gt = _inputs(T, d, torch.bfloat16, False, True, "channel", 4)
