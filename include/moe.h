@@ -601,7 +601,9 @@ int moe_grouped_ffn_fwd_fp8(const uint8_t *x, const uint8_t *x_scale, const int3
  * (dtype).  rstd_post, rstd_pre: [T] fp32, r(y) and r(out) (out, or NULL).
  * out may be x, n may be y; else no two tensors may overlap.  d a multiple of
  * 8, at most 16384; T below 2^26, and T times the row's waves (up to 16) below
- * 2^26 too.
+ * 2^26 too (MOE_ERR_UNSUPPORTED).  Null or misaligned pointers, a norm's rstd or
+ * n without its weight, a gate that does not go with gate_kind, eps <= 0:
+ * MOE_ERR_INVALID_ARG, nothing launched.
  */
 #define MOE_GATE_NONE    0
 #define MOE_GATE_CHANNEL 1
@@ -647,7 +649,9 @@ int moe_residual_norm_bwd(const void *d_out, const void *d_n, const void *out, c
  *                weights[t*k+j] y_perm[slot_to_row[t*k+j]])
  * y_perm: [R,d].  A slot_to_row entry outside [0,R) has no row and adds
  * nothing; what y_perm holds for rows that no slot names is not read.
- * weights: [T,k] fp32, by slot.
+ * weights: [T,k] fp32, by slot.  T*k below 2^31, T times a row's pieces of 2 KB
+ * below 2^26.  Sizes outside of what a call takes: MOE_ERR_UNSUPPORTED; null
+ * or misaligned pointers: MOE_ERR_INVALID_ARG; nothing is launched then.
  */
 int moe_combine_weighted(const void *y_perm, int64_t R, const int32_t *slot_to_row,
                          const float *weights, int dtype, int64_t T, int d, int k, void *y,
@@ -704,6 +708,7 @@ int moe_combine_residual_norm(const void *y_perm, int64_t R, const int32_t *slot
  *   key = mix(mix(mix(mix(seed & 0xffffffff) ^ seed >> 32) ^ step) ^ i) ^ (e >> 32)
  *   r   = mix(key ^ (e & 0xffffffff)) for element e of tensors[i];
  * p takes r's low half, m its high half, v the high half of r * 0x30e9132d.
+ * 0 <= beta < 1, eps in [1e-30, 1e30), lr and weight_decay finite.
  * step: 1, 2, ... below 2^32.  lr_dev (fp32) and step_dev (int64), both or
  * neither: the learning rate and the step count are read from the device, for
  * a captured step; lr and step are not used, and 1-beta^step is formed in fp32.
