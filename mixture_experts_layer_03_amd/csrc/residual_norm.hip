@@ -542,8 +542,14 @@ BwdPlan bwd_plan(int64_t T, int d, int dtype) {
 template <typename T, bool GATHER>
 void launch_fwd(const FwdArgs &a, hipStream_t s) {
   const int nvec = a.d / kVec<T>;
-  // a wave for each row once they fill the card and a row fits its registers
-  if (nvec <= 64 * 8 && a.T >= 2048) {
+  // A wave for each row once they fill the card and a row fits its registers
+  // (us a block : a wave, dense rows of 2880: 1024 rows 5.8 : 7.6, 2048 12.1 :
+  // 9.5, 32768 140 : 130; eight expert rows of 2048 for each of 32768 tokens
+  // 261 : 254, of 4096 33.1 : 35.5), and where a lane holds one piece of it
+  // (rows of 512: 16 of them 2.9 : 2.7, 16384 14.2 : 13.8).  The combined call
+  // goes by the same rule as the two calls that it stands for, so that its sums
+  // are theirs.
+  if (nvec <= 64 || (nvec <= 64 * 8 && a.T >= 2048)) {
     const unsigned grid = (unsigned)((a.T + 3) / 4);
     const int nv = (nvec + 63) / 64;
     if (nv <= 1) k_residual_norm<T, 1, false, GATHER><<<grid, 256, 0, s>>>(a);
