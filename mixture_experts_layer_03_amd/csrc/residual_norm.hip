@@ -592,7 +592,9 @@ int check_common(const char *fn, int64_t T, int d, int dtype, const void *gate, 
               MOE_ERR_UNSUPPORTED, "%s: too many tokens (T=%lld d=%d)", fn, (long long)T, d);
   MOE_REQUIRE(gate_kind >= kGateNone && gate_kind <= kGateElement, MOE_ERR_INVALID_ARG,
               "%s: gate_kind %d", fn, gate_kind);
-  MOE_REQUIRE((gate != nullptr) == (gate_kind != kGateNone) || T == 0, MOE_ERR_INVALID_ARG,
+  // a gate of [T,1] or [T,d] without elements has no address; a channel's always has its d
+  MOE_REQUIRE((gate != nullptr) == (gate_kind != kGateNone) || (T == 0 && gate_kind != kGateChannel),
+              MOE_ERR_INVALID_ARG,
               "%s: gate and gate_kind %d do not go together", fn, gate_kind);
   MOE_REQUIRE(eps_or_one > 0.0f, MOE_ERR_INVALID_ARG, "%s: eps must be positive", fn);
   return MOE_OK;

@@ -1,0 +1,22 @@
+"""The edges of the calls around the block that are decided on the host (no GPU needed)."""
+import ctypes
+
+import pytest
+
+from mixture_experts_layer_03_amd import abi
+
+P = ctypes.c_void_p(0x1000)      # never dereferenced
+N = None
+INVALID, UNSUPPORTED = -1, -2
+
+
+def _bwd(T=4, d=64, gate=N, kind=0, dwp=P, dg=N):
+    return abi.lib().moe_residual_norm_bwd(P, P, P, P, gate, kind, P, P, P, P, 1.0, 1, T, d, P, P, dwp, P, dg, P, 1 << 30, N)
+
+
+@pytest.mark.parametrize("dwp,dg", [(P, P), (N, P), (P, N)])
+def test_a_channels_gate_is_not_empty_without_tokens(dwp, dg):
+    """[d] values, which the weights' gradients are formed with also where there are no rows."""
+    assert _bwd(T=0, kind=1, gate=N, dwp=dwp, dg=dg) == INVALID
+    assert b"gate" in abi.lib().moe_last_error()
+    assert abi.lib().moe_residual_norm(P, P, N, 1, P, P, 1.0, 1e-6, 1, 0, 64, P, P, P, P, N) == INVALID
