@@ -506,7 +506,8 @@ __global__ __launch_bounds__(1024) void k_norm_weights(const BwdArgs a, int bloc
     if ((int)blockIdx.y == a.c_pre) {
       d_pre[c] = s;
     } else {
-      if (d_post) d_post[c] = d_gate ? s * Store<T>::load((const T *)a.gate + c) : s;
+      // asked for alone, d_w_post still has the gate in it
+      if (d_post) d_post[c] = a.gate_kind == kGateChannel ? s * Store<T>::load((const T *)a.gate + c) : s;
       if (d_gate) d_gate[c] = a.w_post ? s * Store<T>::load((const T *)a.w_post + c) : s;
     }
   }
