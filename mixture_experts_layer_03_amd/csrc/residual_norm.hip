@@ -486,7 +486,8 @@ __global__ __launch_bounds__(1024) void k_residual_norm_bwd_long(const BwdArgs a
 
 // The partial sums of `blocks` blocks in a fixed order: a block of 16 waves
 // takes 64 columns, wave w blocks w, w + 16, ...  A channel's d_w_post and
-// d_gate are the one sum times the other's factor.
+// d_gate are the one sum times the other's factor; without rows (blocks 0) the
+// sums are zero whatever the factors hold.
 template <typename T>
 __global__ __launch_bounds__(1024) void k_norm_weights(const BwdArgs a, int blocks, float *d_pre,
                                                        float *d_post, float *d_gate) {
@@ -507,8 +508,8 @@ __global__ __launch_bounds__(1024) void k_norm_weights(const BwdArgs a, int bloc
       d_pre[c] = s;
     } else {
       // asked for alone, d_w_post still has the gate in it
-      if (d_post) d_post[c] = a.gate_kind == kGateChannel ? s * Store<T>::load((const T *)a.gate + c) : s;
-      if (d_gate) d_gate[c] = a.w_post ? s * Store<T>::load((const T *)a.w_post + c) : s;
+      if (d_post) d_post[c] = a.gate_kind == kGateChannel && blocks ? s * Store<T>::load((const T *)a.gate + c) : s;
+      if (d_gate) d_gate[c] = a.w_post && blocks ? s * Store<T>::load((const T *)a.w_post + c) : s;
     }
   }
 }
