@@ -325,7 +325,8 @@ __global__ __launch_bounds__(512) void k_residual_norm_bwd(const BwdArgs a) {
     }
     row_sum<true, 3, 8>(s, lds);
     const float c1 = rn * inv_d * s[0] * rn * rn;   // in this order a row of zeros gives 0
-    const float dot = fmaf(-c1, s[2], s[1]);              // sum(A D), without a token's gate
+    // sum(A D), without a token's gate; where there is no second norm, an infinite y times its zeros is left out
+    const float dot = a.w_pre ? fmaf(-c1, s[2], s[1]) : s[1];
     const float c2 = a.w_post ? rp * inv_d * r.gt * dot * rp * rp : 0.0f;
     if (kToken && a.d_gate && li == 0) ((float *)a.d_gate)[t] = rp * dot;
     const float rpg = rp * r.gt;
@@ -347,7 +348,7 @@ __global__ __launch_bounds__(512) void k_residual_norm_bwd(const BwdArgs a) {
         const float yn = y[i] * rpg;
         const float P = kElement ? D * g[i] : D;
         dx[i] = a.scale * D;
-        dy[i] = fmaf(P * w2[i], rpg, -c2 * y[i]);
+        dy[i] = fmaf(P * w2[i], rpg, a.w_post ? -c2 * y[i] : 0.0f);   // no y in it without its norm
         if (kElement) dg[i] = D * yn * w2[i];
         g_pre[h][i] = fmaf(dn[i], rn * o[i], g_pre[h][i]);
         g_post[h][i] = fmaf(P, yn, g_post[h][i]);
@@ -453,7 +454,7 @@ __global__ __launch_bounds__(1024) void k_residual_norm_bwd_long(const BwdArgs a
       }
     }
     row_sum<true, 3>(s, part[flip]);
-    const float c1 = rn * inv_d * s[0] * rn * rn, dot = fmaf(-c1, s[2], s[1]);
+    const float c1 = rn * inv_d * s[0] * rn * rn, dot = a.w_pre ? fmaf(-c1, s[2], s[1]) : s[1];
     const float c2 = a.w_post ? rp * inv_d * gt * dot * rp * rp : 0.0f, rpg = rp * gt;
     if (kToken && a.d_gate && threadIdx.x == 0) ((float *)a.d_gate)[t] = rp * dot;
     const int64_t row = t * a.d;
@@ -466,7 +467,7 @@ __global__ __launch_bounds__(1024) void k_residual_norm_bwd_long(const BwdArgs a
         const float D = fmaf(-c1, p.o[i], fmaf(rn, p.dn[i] * p.w1[i], p.dd[i]));
         const float yn = p.y[i] * rpg, P = kElement ? D * p.g[i] : D;
         dx[i] = a.scale * D;
-        dy[i] = fmaf(P * p.w2[i], rpg, -c2 * p.y[i]);
+        dy[i] = fmaf(P * p.w2[i], rpg, a.w_post ? -c2 * p.y[i] : 0.0f);
         if (kElement) dg[i] = D * yn * p.w2[i];
         acc[0][c * N + i] = fmaf(p.dn[i], rn * p.o[i], acc[0][c * N + i]);
         acc[1][c * N + i] = fmaf(P, yn, acc[1][c * N + i]);
