@@ -214,15 +214,39 @@ __device__ __forceinline__ void adamw_block(const AdamArgs<4 + (MASTER ? 1 : 0) 
     step_size = lr / -expm1f((float)s * a.ln_b1);
     rbc2 = 1.0f / sqrtf(-expm1f((float)s * a.ln_b2));
   }
+  // The root instruction takes what is below 2^-126 for zero, and eps may be
+  // far below the root of that: there it is the root of v 2^64.
+  auto lifted_root = [&](int e) {
+    const bool low = v[e] < 0x1p-126f;
+    return __builtin_amdgcn_sqrtf(low ? v[e] * 0x1p64f : v[e]) * (low ? 0x1p-32f : 1.0f);
+  };
 #pragma unroll
   for (int e = 0; e < V; ++e) {
     const float ge = g[e] * gs;
     m[e] = m[e] * a.b1 + ge * a.a1;
     v[e] = v[e] * a.b2 + ge * a.a2 * ge;
     // 1-ulp root and reciprocal: off by 2^-22 of the update, below the
-    // rounding of p wherever the update is below p/4
-    const float den = fmaf(__builtin_amdgcn_sqrtf(v[e]), rbc2, a.eps);
+    // rounding of p wherever the update is below p/4.  (In this loop: from a
+    // function of its own the loads come out in another order, and 796M
+    // elements take 3.85 ms for 3.78.)
+    const float den = fmaf(EIGHT ? __builtin_amdgcn_sqrtf(v[e]) : lifted_root(e), rbc2, a.eps);
     p[e] = fmaf(-step_size, m[e] * __builtin_amdgcn_rcpf(den), p[e] * decay);
+  }
+  if constexpr (EIGHT) {
+    // Here the choice for each element would cost every step (604M weights
+    // 1165 -> 1224 us); where a v is that low and not zero, p is read again.
+    uint32_t least = ~0u;
+#pragma unroll
+    for (int e = 0; e < V; ++e) least = min(least, __float_as_uint(v[e]) - 1u);
+    if (__any(least < 0x7fffffu)) {
+      if constexpr (MASTER) load_row<TAIL, float>(t_master, i, n, p);
+      else load_row<TAIL, P>(t_p, i, n, p);
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float den = fmaf(lifted_root(e), rbc2, a.eps);
+        p[e] = fmaf(-step_size, m[e] * __builtin_amdgcn_rcpf(den), p[e] * decay);
+      }
+    }
   }
 
   // The conversions below round a magnitude up where the bits that it loses
