@@ -109,10 +109,12 @@ class AdamW:
     def step(self, grads, grad_scale=None, stream=None):
         """One step in place.  grads: a tensor for each parameter, all fp32 or (bf16 parameters)
         all bf16; grad_scale: an fp32 device tensor of one element that multiplies them, or None.
-        Everything runs on `stream` (the current one); with capturable that has to be the current
-        one, since the count is stepped there (``step_dev``; ``steps`` counts calls, not replays)."""
+        Everything runs on `stream` (the current one); with capturable another one is refused,
+        since the count is stepped on the current one (``step_dev``; ``steps`` counts calls, not replays)."""
         if len(grads) != len(self.params):
             raise ValueError("AdamW: %d gradients for %d parameters" % (len(grads), len(self.params)))
+        if self.step_dev is not None and stream is not None and stream != abi._stream(None):
+            raise ValueError("AdamW: a capturable step runs on the current stream, which steps its count")
         dtype, device = grads[0].dtype, self.device
         gcode = abi._dtype_code(grads[0])
         if device.type != "cuda" or device.index != torch.cuda.current_device():
