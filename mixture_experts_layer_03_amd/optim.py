@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 from array import array
+from collections import OrderedDict
 from operator import attrgetter
 
 import torch
@@ -34,14 +35,33 @@ def state_shapes(numel: int, state_bits: int):
             "m_scale": (blocks, torch.uint8), "v_scale": (blocks, torch.uint8)}
 
 
+class States(OrderedDict):
+    """{name: the tensors}: other tensors in their place would not reach the kernel, so none are taken.
+    Pickled and copied it is an OrderedDict."""
+
+    def _fixed(self, *args, **kw):
+        raise TypeError("AdamW: states are loaded with load_state, or copied into in place")
+
+    __setitem__ = __delitem__ = update = pop = popitem = clear = setdefault = __ior__ = _fixed
+
+    def __init__(self, items):
+        for name, tensors in items:
+            super().__setitem__(name, tensors)
+
+    def __reduce__(self):
+        return OrderedDict, (), None, None, iter(self.items())
+
+
 class AdamW:
     """params: contiguous bf16 or fp32 tensors, all of one type and on one device.
 
     masters: True for fp32 copies made here, or a list of them; state: a dict
     of lists of tensors (as ``self.state``) to go on from, with ``step`` its
-    step count.  weight_decay: one number or one for each tensor.  capturable:
-    the step count and the learning rate live on the device, so that a captured
-    step() counts on when it is replayed; ``set_lr`` changes the rate."""
+    step count.  Given tensors are stepped in place; ``state`` and ``masters``
+    show them, and load_state copies into them.  weight_decay: one number or one
+    for each tensor.  capturable: the step count and the learning rate live on
+    the device, so that a captured step() counts on when it is replayed;
+    ``set_lr`` changes the rate."""
 
     def __init__(self, params, lr, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01,
                  state_bits: int = 32, masters=None, seed: int = 0, step: int = 0, state=None,
@@ -62,8 +82,10 @@ class AdamW:
         self.seed, self.steps = int(seed) & 0xFFFFFFFFFFFFFFFF, int(step)
         if masters is True:
             masters = [p.float() for p in self.params]
-        self.masters = list(masters) if masters else None
-        if self.masters is not None and self.dtype != torch.bfloat16:
+        # The kernel has the states' addresses: tensor objects of their own keep that memory, whatever
+        # becomes of the caller's.
+        self._masters = [t.detach() for t in masters] if masters else None
+        if self._masters is not None and self.dtype != torch.bfloat16:
             raise ValueError("AdamW: only bf16 parameters have fp32 copies")
         names = state_shapes(0, state_bits)
         if state is None:
@@ -72,21 +94,21 @@ class AdamW:
                 for n, (count, dt) in state_shapes(p.numel(), state_bits).items():
                     t = torch.zeros(count, dtype=dt, device=self.device)
                     state[n].append(t.fill_(127) if dt == torch.uint8 else t)
-        self.state = {n: list(state[n]) for n in names}
+        self._state = {n: [t.detach() for t in state[n]] for n in names}
         for i, p in enumerate(self.params):
             for n, (count, dt) in state_shapes(p.numel(), state_bits).items():
-                self._need(n, i, self.state[n][i], count, dt)
-            if self.masters is not None:
-                self._need("master", i, self.masters[i], p.numel(), torch.float32)
+                self._need(n, i, self._state[n][i], count, dt)
+            if self._masters is not None:
+                self._need("master", i, self._masters[i], p.numel(), torch.float32)
         self._table = (abi.AdamwTensor * len(self.params))()
         for i, p in enumerate(self.params):
             t = self._table[i]
             t.param, t.numel, t.weight_decay = p.data_ptr(), p.numel(), float(decay[i])
-            t.m, t.v = self.state["m"][i].data_ptr(), self.state["v"][i].data_ptr()
+            t.m, t.v = self._state["m"][i].data_ptr(), self._state["v"][i].data_ptr()
             if state_bits == 8:
-                t.m_scale, t.v_scale = self.state["m_scale"][i].data_ptr(), self.state["v_scale"][i].data_ptr()
-            if self.masters is not None:
-                t.master = self.masters[i].data_ptr()
+                t.m_scale, t.v_scale = self._state["m_scale"][i].data_ptr(), self._state["v_scale"][i].data_ptr()
+            if self._masters is not None:
+                t.master = self._masters[i].data_ptr()
         self._shapes = [p.shape for p in self.params]
         self._pointers = [p.data_ptr() for p in self.params]
         words = ctypes.sizeof(abi.AdamwTensor) // 8
@@ -95,6 +117,37 @@ class AdamW:
         if capturable:
             self.lr_dev = torch.full((1,), self.lr, dtype=torch.float32, device=self.device)
             self.step_dev = torch.full((1,), self.steps, dtype=torch.int64, device=self.device)
+
+    @property
+    def state(self):
+        """{name: a tensor for each parameter}; what is written into them is what the next step reads."""
+        return States((n, tuple(t.detach() for t in ts)) for n, ts in self._state.items())
+
+    @property
+    def masters(self):
+        """The fp32 copies, a tensor for each parameter, or None."""
+        return None if self._masters is None else tuple(t.detach() for t in self._masters)
+
+    def load_state(self, state, step: int, masters=None):
+        """Goes on from a state (as ``state``) and masters of the same sizes, on any device, after `step` steps."""
+        if (masters is None) != (self._masters is None):
+            raise ValueError("AdamW: masters go with an optimizer that has them")
+        pairs = [(n, ts, state.get(n, ())) for n, ts in self._state.items()]
+        if masters is not None:
+            pairs.append(("master", self._masters, masters))
+        for what, to, given in pairs:
+            if len(given) != len(to):
+                raise ValueError("AdamW: %s of %d tensors for %d parameters" % (what, len(given), len(to)))
+            for i, (t, f) in enumerate(zip(to, given)):
+                if f.numel() != t.numel() or f.dtype != t.dtype:
+                    raise ValueError("AdamW: %s %d must be %d of %s, not %d of %s"
+                                     % (what, i, t.numel(), t.dtype, f.numel(), f.dtype))
+        for _, to, given in pairs:
+            for t, f in zip(to, given):
+                t.copy_(f.reshape(t.shape))
+        self.steps = int(step)
+        if self.step_dev is not None:
+            self.step_dev.fill_(self.steps)
 
     def _need(self, what, i, t, numel, dtype):
         if t.numel() != numel or t.dtype != dtype or t.device != self.device or not t.is_contiguous():
