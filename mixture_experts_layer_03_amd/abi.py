@@ -601,6 +601,9 @@ def moe_residual_norm_bwd(d_out, d_n, out, y, d_x, d_y, ws, w_post=None, w_pre=N
           ("rstd_post rstd_pre", (rstd_post, rstd_pre), (T,), f32),
           ("d_w_post d_w_pre", (d_w_post, d_w_pre), (d,), f32),
           ("d_gate", (d_gate,), gshape, f32 if kind == MOE_GATE_CHANNEL else gtype))
+    if ws is not None and (ws.get_device() != here or not ws.is_contiguous()):
+        raise ValueError("%s: ws must be contiguous and on the current device, not %s%s on %s"
+                         % (fn, tuple(ws.shape), "" if ws.is_contiguous() else " with strides", ws.device))
     _check(fn, lib().moe_residual_norm_bwd(
         _p(d_out), _p(d_n), _p(out), _p(y), _p(gate), kind, _p(w_post), _p(w_pre), _p(rstd_post),
         _p(rstd_pre), res_scale, _dtype_code(some), T, d, _p(d_x), _p(d_y), _p(d_w_post),
