@@ -600,8 +600,8 @@ int moe_grouped_ffn_fwd_fp8(const uint8_t *x, const uint8_t *x_scale, const int3
  * MOE_GATE_NONE NULL, _CHANNEL [d] (dtype), _TOKEN [T] fp32, _ELEMENT [T,d]
  * (dtype).  rstd_post, rstd_pre: [T] fp32, r(y) and r(out) (out, or NULL).
  * out may be x, n may be y; else no two tensors may overlap.  d a multiple of
- * 8, at most 16384; T below 2^26, and T times the row's waves (up to 16) below
- * 2^26 too (MOE_ERR_UNSUPPORTED).  Null or misaligned pointers, a norm's rstd or
+ * 8, at most 16384; T at most 2^26 - 4 (the gradient: 2^26 - 1), and T times the
+ * row's waves (up to 16) below 2^26 too (MOE_ERR_UNSUPPORTED).  Null or misaligned pointers, a norm's rstd or
  * n without its weight, a gate that does not go with gate_kind, eps <= 0:
  * MOE_ERR_INVALID_ARG, nothing launched.
  */

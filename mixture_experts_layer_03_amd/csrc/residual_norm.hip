@@ -606,6 +606,8 @@ int check_common(const char *fn, int64_t T, int d, int dtype, const void *gate, 
 int run_fwd(const char *fn, const FwdArgs &a, bool gather, int dtype, void *stream) {
   const int rc = check_common(fn, a.T, a.d, dtype, a.gate, a.gate_kind, a.eps);
   if (rc != MOE_OK) return rc;
+  // four rows to a block of 256 threads
+  MOE_REQUIRE((a.T + 3) / 4 < ((int64_t)1 << 24), MOE_ERR_UNSUPPORTED, "%s: too many tokens (T=%lld)", fn, (long long)a.T);
   if (gather) {
     MOE_REQUIRE(a.R >= 0 && a.k >= 1 && a.k <= kMaxTopK && a.T * a.k < ((int64_t)1 << 31),
                 MOE_ERR_INVALID_ARG, "%s: bad sizes (T=%lld k=%d R=%lld)", fn, (long long)a.T, a.k,

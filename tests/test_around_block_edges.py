@@ -20,3 +20,11 @@ def test_a_channels_gate_is_not_empty_without_tokens(dwp, dg):
     assert _bwd(T=0, kind=1, gate=N, dwp=dwp, dg=dg) == INVALID
     assert b"gate" in abi.lib().moe_last_error()
     assert abi.lib().moe_residual_norm(P, P, N, 1, P, P, 1.0, 1e-6, 1, 0, 64, P, P, P, P, N) == INVALID
+
+
+@pytest.mark.parametrize("T", [(1 << 26) - 1, (1 << 26) - 3])
+def test_norms_of_as_many_tokens_as_a_launch_has_no_threads_for(T):
+    """Four rows of a wave each to a block: (T + 3) / 4 blocks of 256 threads, below 2^32 of them."""
+    f = abi.lib()
+    assert f.moe_residual_norm(P, P, N, 0, P, P, 1.0, 1e-6, 1, T, 8, P, P, P, P, N) == UNSUPPORTED
+    assert f.moe_combine_residual_norm(P, 8, P, P, 1, P, N, 0, P, P, 1.0, 1e-6, 1, T, 8, N, P, P, P, P, N) == UNSUPPORTED
