@@ -664,7 +664,7 @@ int moe_combine_weighted(const void *y_perm, int64_t R, const int32_t *slot_to_r
  * [R,d], d_row_scale [R].  Rows that no
  * slot names are left as they were.  dy_perm or d_row_scale may be NULL, y_perm too
  * where d_row_scale is; dy_perm may not overlap y_perm.  No two slots may
- * name the same row.  T*k below 2^26.
+ * name the same row.  T*k at most 2^26 - 4.
  */
 int moe_combine_weighted_bwd(const void *dy, const void *y_perm, int64_t R,
                              const int32_t *slot_to_row, const float *weights, int dtype, int64_t T,

@@ -163,18 +163,17 @@ int moe_combine_weighted_bwd(const void *dy, const void *y_perm, int64_t R,
   MOE_REQUIRE(dy && slot_to_row && weights && (dy_perm || d_row_scale) && (y_perm || !d_row_scale),
               MOE_ERR_INVALID_ARG, "%s: null pointer", fn);
   MOE_REQUIRE(aligned16(dy) && aligned16(y_perm) && aligned16(dy_perm), MOE_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", fn);
-  const int64_t slots = T * k;
-  MOE_REQUIRE(slots < ((int64_t)1 << 26), MOE_ERR_UNSUPPORTED, "%s: too many rows (T=%lld k=%d)",
+  const int64_t slots = T * k, blocks = (slots + 3) / 4;
+  MOE_REQUIRE(blocks < ((int64_t)1 << 24), MOE_ERR_UNSUPPORTED, "%s: too many rows (T=%lld k=%d)",
               fn, (long long)T, k);   // a launch has below 2^32 threads
   hipStream_t s = (hipStream_t)stream;
-  const unsigned blocks = (unsigned)((slots + 3) / 4);
   MOE_LAUNCH("combine_weighted_bwd", s, {
     if (dtype == MOE_BF16)
-      k_combine_weighted_bwd<bf16_t><<<blocks, 256, 0, s>>>(
+      k_combine_weighted_bwd<bf16_t><<<(unsigned)blocks, 256, 0, s>>>(
           (const bf16_t *)dy, (const bf16_t *)y_perm, slot_to_row, weights, slots, R, d, k,
           (bf16_t *)dy_perm, d_row_scale);
     else
-      k_combine_weighted_bwd<float><<<blocks, 256, 0, s>>>(
+      k_combine_weighted_bwd<float><<<(unsigned)blocks, 256, 0, s>>>(
           (const float *)dy, (const float *)y_perm, slot_to_row, weights, slots, R, d, k,
           (float *)dy_perm, d_row_scale);
   });

@@ -28,3 +28,9 @@ def test_norms_of_as_many_tokens_as_a_launch_has_no_threads_for(T):
     f = abi.lib()
     assert f.moe_residual_norm(P, P, N, 0, P, P, 1.0, 1e-6, 1, T, 8, P, P, P, P, N) == UNSUPPORTED
     assert f.moe_combine_residual_norm(P, 8, P, P, 1, P, N, 0, P, P, 1.0, 1e-6, 1, T, 8, N, P, P, P, P, N) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("T,k", [((1 << 26) - 1, 1), ((1 << 26) - 3, 1), (22369621, 3)])
+def test_a_combines_gradient_of_as_many_slots_as_a_launch_has_no_threads_for(T, k):
+    assert T * k in range((1 << 26) - 3, 1 << 26)
+    assert abi.lib().moe_combine_weighted_bwd(P, P, 8, P, P, 1, T, 8, k, P, P, N) == UNSUPPORTED

@@ -23,3 +23,22 @@ def test_norms_of_the_most_tokens():
         abi.moe_residual_norm(x[s].clone(), None, None, m, w_pre=w, rstd_pre=q)
         assert torch.equal(m, n[s]) and torch.equal(q, r[s])
     assert (r > 0).all() and torch.isfinite(n).all()
+
+
+def test_gradient_of_the_most_slots():
+    """2^26 - 4 slots of rows of one piece, in an order of their own: every row against its token's and its weight's."""
+    T, k, d = (1 << 24) - 1, 4, 8
+    R = T * k
+    g = torch.Generator(device=DEV).manual_seed(2)
+    dy = torch.empty(T, d, dtype=BF, device=DEV).normal_(generator=g)
+    y_perm = torch.ones(R, d, dtype=BF, device=DEV)
+    w = 2.0 ** torch.randint(-2, 3, (T, k), generator=g, device=DEV).float()
+    rows = torch.arange(R - 1, -1, -1, dtype=torch.int32, device=DEV)
+    dyp, drs = torch.empty_like(y_perm), torch.empty(R, device=DEV)
+    abi.moe_combine_weighted_bwd(dy, y_perm, rows, w, dyp, drs)
+    back = dyp.flip(0).view(T, k, d)                    # powers of two: products are exact
+    assert torch.equal(back, (dy[:, None, :].float() * w[:, :, None]).to(BF))
+    want = dy.double().sum(1, keepdim=True).expand(T, k)
+    # 8 addends in a lane's chain: 8 roundings of 2^-24 of the sum of their sizes
+    size = dy.double().abs().sum(1, keepdim=True)
+    assert ((drs.flip(0).view(T, k).double() - want).abs() <= 8 * 2.0 ** -24 * size).all()
