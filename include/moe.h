@@ -649,9 +649,10 @@ int moe_residual_norm_bwd(const void *d_out, const void *d_n, const void *out, c
  *                weights[t*k+j] y_perm[slot_to_row[t*k+j]])
  * y_perm: [R,d].  A slot_to_row entry outside [0,R) has no row and adds
  * nothing; what y_perm holds for rows that no slot names is not read.
- * weights: [T,k] fp32, by slot.  T*k below 2^31, T times a row's pieces of 2 KB
- * below 2^26.  Sizes outside of what a call takes: MOE_ERR_UNSUPPORTED; null
- * or misaligned pointers: MOE_ERR_INVALID_ARG; nothing is launched then.
+ * weights: [T,k] fp32, by slot.  d a multiple of 8, a row below 2^31 bytes; T*k
+ * below 2^31, T times a row's pieces of 2 KB at most 2^26 - 4.  Sizes outside of
+ * what a call takes: MOE_ERR_UNSUPPORTED; null or misaligned pointers or sizes
+ * below 0: MOE_ERR_INVALID_ARG; nothing is launched then.
  */
 int moe_combine_weighted(const void *y_perm, int64_t R, const int32_t *slot_to_row,
                          const float *weights, int dtype, int64_t T, int d, int k, void *y,

@@ -117,6 +117,9 @@ int check(const char *fn, int64_t T, int64_t R, int d, int k, int dtype) {
   MOE_REQUIRE(k >= 1 && k <= kMaxTopK, MOE_ERR_UNSUPPORTED, "%s: k=%d", fn, k);
   MOE_REQUIRE(T < ((int64_t)1 << 31) / k, MOE_ERR_UNSUPPORTED, "%s: T*k >= 2^31", fn);
   MOE_REQUIRE(dtype == MOE_BF16 || dtype == MOE_F32, MOE_ERR_UNSUPPORTED, "%s: dtype %d", fn, dtype);
+  // places in a row, and up to 6 KB past its end, are 32 bits of bytes in the kernels
+  MOE_REQUIRE((int64_t)d * (dtype == MOE_BF16 ? 2 : 4) < ((int64_t)1 << 31), MOE_ERR_UNSUPPORTED,
+              "%s: rows of 2^31 bytes and more (d=%d)", fn, d);
   return MOE_OK;
 }
 

@@ -34,3 +34,12 @@ def test_norms_of_as_many_tokens_as_a_launch_has_no_threads_for(T):
 def test_a_combines_gradient_of_as_many_slots_as_a_launch_has_no_threads_for(T, k):
     assert T * k in range((1 << 26) - 3, 1 << 26)
     assert abi.lib().moe_combine_weighted_bwd(P, P, 8, P, P, 1, T, 8, k, P, P, N) == UNSUPPORTED
+
+
+# (the last: 16 bytes short of 2^32, where a counter in steps of some KB never passes the end)
+@pytest.mark.parametrize("dtype,d", [(0, 1 << 29), (0, 1 << 30), (1, 1 << 30), (0, (1 << 30) - 8), (1, (1 << 31) - 8)])
+def test_rows_of_2_gb(dtype, d):
+    """Places in a row are counted in 32 bits of bytes."""
+    f, b = abi.lib().moe_combine_weighted, abi.lib().moe_combine_weighted_bwd
+    assert f(P, 8, P, P, dtype, 1, d, 1, P, N) == UNSUPPORTED
+    assert b(P, P, 8, P, P, dtype, 1, d, 1, P, P, N) == UNSUPPORTED
