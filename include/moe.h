@@ -651,7 +651,7 @@ int moe_residual_norm_bwd(const void *d_out, const void *d_n, const void *out, c
  * nothing; what y_perm holds for rows that no slot names is not read.
  * weights: [T,k] fp32, by slot.  d a multiple of 8, a row below 2^31 bytes; T*k
  * below 2^31, T times a row's pieces of 2 KB at most 2^26 - 4.  Sizes outside of
- * what a call takes: MOE_ERR_UNSUPPORTED; null or misaligned pointers or sizes
+ * what a call takes: MOE_ERR_UNSUPPORTED; null or misaligned pointers, T or R
  * below 0: MOE_ERR_INVALID_ARG; nothing is launched then.
  */
 int moe_combine_weighted(const void *y_perm, int64_t R, const int32_t *slot_to_row,

@@ -404,6 +404,7 @@ class ResidualMoE:
             self.d_w_post = z(d, dt=f32) if post_norm else None
             self.d_w_next = z(d, dt=f32) if next_norm else None
             self.d_gate = None
+            self._d_gates = {}     # by shape and type: a captured backward goes on writing its own
             self.ws = torch.empty(max(256, abi.moe_residual_norm_bwd_workspace_size(T, d)),
                                   dtype=torch.uint8, device=blk.device)
 
@@ -433,8 +434,10 @@ class ResidualMoE:
         b = self.blk
         if gate is not None:
             dt = torch.float32 if gate.dim() == 1 else gate.dtype
-            if self.d_gate is None or self.d_gate.shape != gate.shape or self.d_gate.dtype != dt:
-                self.d_gate = torch.empty(gate.shape, dtype=dt, device=b.device)
+            key = (gate.shape, dt)
+            if key not in self._d_gates:
+                self._d_gates[key] = torch.empty(gate.shape, dtype=dt, device=b.device)
+            self.d_gate = self._d_gates[key]
         abi.moe_residual_norm_bwd(d_out, d_n, self.out, b.y, self.d_x, self.d_y, self.ws, w_post=w_post,
                                   w_pre=w_next, gate=gate, res_scale=self.res_scale,
                                   rstd_post=self.rstd_post, rstd_pre=self.rstd_next,
