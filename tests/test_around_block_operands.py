@@ -56,3 +56,77 @@ def test_a_workspace_on_another_device(lib, monkeypatch):
     with pytest.raises(ValueError, match="ws must be contiguous and on the current device"):
         abi.moe_residual_norm_bwd(**dict(_bwd_args(), ws=ws.as_subclass(elsewhere)))
     assert not lib.calls
+
+
+def _fwd_args():
+    rows = lambda: _z(T, D)
+    return dict(x=rows(), y=rows(), out=rows(), n=rows(), w_post=_z(D), w_pre=_z(D), gate=_z(D), rstd_post=_z(T, dt=F32),
+                rstd_pre=_z(T, dt=F32))
+
+
+CALLS = {
+    "moe_residual_norm": _fwd_args,
+    "moe_residual_norm_bwd": _bwd_args,
+    "moe_combine_weighted": lambda: dict(y_perm=_z(R, D), slot_to_row=_z(T * K, dt=I32), weights=_z(T, K, dt=F32), y=_z(T, D)),
+    "moe_combine_weighted_bwd": lambda: dict(dy=_z(T, D), y_perm=_z(R, D), slot_to_row=_z(T * K, dt=I32), weights=_z(T, K, dt=F32),
+                                             dy_perm=_z(R, D), d_row_scale=_z(R, dt=F32)),
+    "moe_combine_residual_norm": lambda: dict(_fwd_args(), y_perm=_z(R, D), slot_to_row=_z(T * K, dt=I32), weights=_z(T, K, dt=F32),
+                                              k=K),
+}
+# what the sizes are taken from: another one makes the others' sizes wrong (their rows or columns are named instead)
+LEADS = {"moe_residual_norm": "y", "moe_residual_norm_bwd": "d_out", "moe_combine_weighted": "y", "moe_combine_weighted_bwd": "dy",
+         "moe_combine_residual_norm": "out"}
+OPERANDS = [(fn, name) for fn, args in CALLS.items() for name, t in args().items() if isinstance(t, torch.Tensor) and name != "ws"]
+
+
+@pytest.mark.parametrize("fn", list(CALLS))
+def test_well_formed_calls_go_through(lib, fn):
+    getattr(abi, fn)(**CALLS[fn]())
+    assert lib.calls == [fn]
+
+
+@pytest.mark.parametrize("fn,name", OPERANDS)
+def test_an_operand_of_another_shape_type_or_stride(lib, fn, name):
+    t = CALLS[fn]()[name]
+    longer = torch.zeros(t.shape[0] + 1, *t.shape[1:], dtype=t.dtype)
+    wider = torch.zeros(*t.shape[:-1], t.shape[-1] + 8, dtype=t.dtype)
+    typed = torch.zeros(t.shape, dtype=torch.float64 if t.dtype != I32 else torch.int64)
+    strided = torch.zeros(*t.shape[:-1], 2 * t.shape[-1], dtype=t.dtype)[..., ::2]
+    assert strided.shape == t.shape and not strided.is_contiguous()
+    # rows of y_perm are free where no other tensor has them
+    free_rows = fn in ("moe_combine_weighted", "moe_combine_residual_norm") and name == "y_perm"
+    for what, bad in (("longer", longer), ("wider", wider), ("typed", typed), ("strided", strided)):
+        if what == "longer" and free_rows:
+            continue
+        leads = name in (LEADS[fn], "weights") and what != "strided"
+        who = r".* must be" if leads else r"(gate must be|%s must be a contiguous)" % name
+        if fn == "moe_combine_weighted_bwd" and name == "y_perm" and what == "longer":
+            who = r"dy_perm must be"
+        with pytest.raises((ValueError, TypeError), match=who):
+            getattr(abi, fn)(**dict(CALLS[fn](), **{name: bad}))
+    assert not lib.calls
+
+
+@pytest.mark.parametrize("fn,name", OPERANDS)
+def test_an_operand_on_another_device(lib, fn, name):
+    elsewhere = type("Elsewhere", (torch.Tensor,), {"get_device": lambda self: 0})
+    args = CALLS[fn]()
+    with pytest.raises(ValueError, match=name + " must be a contiguous .* on the current device"):
+        getattr(abi, fn)(**dict(args, **{name: args[name].as_subclass(elsewhere)}))
+    assert not lib.calls
+
+
+@pytest.mark.parametrize("gate", [(D,), (T, 1), (T, D)])
+@pytest.mark.parametrize("fn", ["moe_residual_norm", "moe_residual_norm_bwd", "moe_combine_residual_norm"])
+def test_gates_by_their_shape(lib, fn, gate):
+    right = F32 if gate == (T, 1) else BF
+    kw = dict(CALLS[fn](), gate=_z(*gate, dt=right))
+    if "d_gate" in kw:
+        kw["d_gate"] = _z(*gate, dt=BF if gate == (T, D) else F32)
+    getattr(abi, fn)(**kw)
+    with pytest.raises(ValueError, match="gate must be a contiguous"):
+        getattr(abi, fn)(**dict(kw, gate=_z(*gate, dt=BF if right is F32 else F32)))
+    for shape in ((T,), (1, D), (D, 1), (T, 2)):
+        with pytest.raises(ValueError, match=r"gate must be \[d\], \[T,1\] or \[T,d\]"):
+            getattr(abi, fn)(**dict(kw, gate=_z(*shape)))
+    assert lib.calls == [fn]

@@ -23,3 +23,42 @@ def test_a_captured_steps_count_is_on_the_current_stream():
         opt.step([g])
     torch.cuda.synchronize()
     assert opt.steps == 3 and int(opt.step_dev) == 3 and not torch.equal(p, keep)
+
+
+def test_gradients_of_another_shape_type_stride_or_device():
+    z = lambda *s, dt=torch.float32: torch.ones(*s, dtype=dt, device=DEV)
+    p = [z(40, 8), z(300)]
+    opt = AdamW(p, lr=1e-2)
+    ok = [z(40, 8), z(300)]
+    opt.step(ok)
+    keep = [t.clone() for t in p]
+    for bad, error, why in (([z(40, 8), z(299)], ValueError, "gradient 1 is"), ([z(8, 40), z(300)], ValueError, "gradient 0 is"),
+                            ([z(320), z(300)], ValueError, "gradient 0 is"),
+                            ([z(8, 40).t(), z(300)], ValueError, "gradient 0 must be contiguous"),
+                            ([z(40, 8), z(600)[::2]], ValueError, "gradient 1 must be contiguous"),
+                            ([z(40, 8), z(300, dt=torch.bfloat16)], ValueError, "gradient 1 must be"),
+                            ([z(40, 8), torch.ones(300)], ValueError, "gradient 1 must be .* on cpu"),
+                            ([z(40, 8, dt=torch.float64), z(300, dt=torch.float64)], TypeError, "dtype"),
+                            ([z(40, 8)], ValueError, "1 gradients for 2 parameters")):
+        with pytest.raises(error, match=why):
+            opt.step(bad)
+    for scale in (torch.ones(1), z(2), z(1, dt=torch.bfloat16)):
+        with pytest.raises(ValueError, match="grad_scale 0 must be"):
+            opt.step(ok, grad_scale=scale)
+    assert opt.steps == 1 and all(torch.equal(a, b) for a, b in zip(p, keep))
+    p[1].data = z(300)
+    with pytest.raises(ValueError, match="a parameter has moved"):
+        opt.step(ok)
+    opt = AdamW([z(300, dt=torch.bfloat16)], lr=1e-2)            # both types of gradients
+    opt.step([z(300)])
+    opt.step([z(300, dt=torch.bfloat16)])
+    with pytest.raises(ValueError, match="parameters are on cpu"):
+        AdamW([torch.ones(300)], lr=1e-2).step([torch.ones(300)])
+
+
+def test_a_moved_parameter_or_replaced_one():
+    p, g = [torch.ones(64, device=DEV) for _ in range(2)], [torch.ones(64, device=DEV) for _ in range(2)]
+    opt = AdamW(p, lr=1e-2)
+    opt.params[1] = torch.ones(64, device=DEV)
+    with pytest.raises(ValueError, match="a parameter has moved"):
+        opt.step(g)
