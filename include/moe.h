@@ -601,9 +601,12 @@ int moe_grouped_ffn_fwd_fp8(const uint8_t *x, const uint8_t *x_scale, const int3
  * (dtype).  rstd_post, rstd_pre: [T] fp32, r(y) and r(out) (out, or NULL).
  * out may be x, n may be y; else no two tensors may overlap.  d a multiple of
  * 8, at most 16384; T at most 2^26 - 4 (the gradient: 2^26 - 1), and T times the
- * row's waves (up to 16) below 2^26 too (MOE_ERR_UNSUPPORTED).  Null or misaligned pointers, a norm's rstd or
- * n without its weight, a gate that does not go with gate_kind, eps <= 0:
- * MOE_ERR_INVALID_ARG, nothing launched.
+ * row's waves (up to 16) below 2^26 too (MOE_ERR_UNSUPPORTED).  Null or
+ * misaligned pointers, a norm's rstd or n without its weight, a gate that does
+ * not go with gate_kind (a channel's also where T = 0), eps <= 0:
+ * MOE_ERR_INVALID_ARG, nothing launched.  The sum of a row's squares is formed
+ * in another order where T is below 2048 (rows of 1 to 8 KB): its last bits
+ * depend on that, and on no other row.
  */
 #define MOE_GATE_NONE    0
 #define MOE_GATE_CHANNEL 1
@@ -674,8 +677,9 @@ int moe_combine_weighted_bwd(const void *dy, const void *y_perm, int64_t R,
 /*
  * moe_combine_weighted (weights NULL: moe_combine) and moe_residual_norm on
  * its rows in one pass, bit for bit what the two calls give: y, the combined
- * rows [T,d], is stored for a backward, or NULL.  Arguments and errors as
- * theirs; y may not overlap another tensor.
+ * rows [T,d], is stored for a backward, or NULL; y may not overlap another
+ * tensor.  Arguments, limits and errors as moe_residual_norm's; R below 0, k
+ * outside of 1 to 32 or T*k of 2^31 and more: MOE_ERR_INVALID_ARG.
  */
 int moe_combine_residual_norm(const void *y_perm, int64_t R, const int32_t *slot_to_row,
                               const float *weights, int k, const void *x, const void *gate,

@@ -351,7 +351,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(EIGHT ? 6 :
   const int64_t i = at + threadIdx.x * V;
   // Whole blocks without the code for ends between their accesses: 8-bit
   // states' instructions are then half as many to fetch when a launch begins
-  // (120 tensors of 28M elements 106 -> 95 us).  With 32-bit states the
+  // (120 tensors of 47M elements 106 -> 95 us).  With 32-bit states the
   // branches between the accesses spread them out, and long tensors take 3.80
   // ms with them, 3.98 without (796M elements).
   if (EIGHT && at + 256 * V <= n) adamw_block<P, G, MASTER, EIGHT, false>(a, lo, i, n);
